@@ -56,7 +56,12 @@ typedef enum {
   PA_ERR_WORKSPACE = 9      /* decode workspace missing or too small         */
 } pa_status;
 
-typedef enum { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
+typedef enum {
+  PA_F32 = 0,
+  PA_BF16 = 1,
+  PA_Q8_INT8 = 2,           /* 8-bit pools: int8 codes, a scale per tile     */
+  PA_Q8_E4M3 = 3            /* 8-bit pools: e4m3 codes, a scale per tile     */
+} pa_dtype;
 
 /* Device error word bits (pa_get_device_error). */
 #define PA_DEVERR_SLOT    1u  /* append: slot >= num_blocks * 16             */
@@ -66,6 +71,8 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_TIMEOUT 8u  /* decode/prefill: a wait for staged data gave
                                  up after 2 s (the kernel returned instead of
                                  hanging)                                    */
+#define PA_DEVERR_NONFINITE 16u /* 8-bit append: a NaN or infinity in k or v
+                                 (stored as 0 or the largest code)           */
 
 /*
  * The KV pool of one attention layer: one contiguous device buffer
@@ -78,8 +85,9 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
  * layout is this library's choice.
  * Token position p of a sequence with block table T lives in slot
  *     slot = T[p / 16] * 16 + p % 16.
- * Supported: block_size 16; head_dim 64 or 128; dtype PA_F32 or PA_BF16;
- * kv_pool 16-byte aligned.
+ * Supported: block_size 16; head_dim 64 or 128; dtype PA_F32 or PA_BF16 (an
+ * 8-bit dtype names the layout of the section "8-bit pools" below, which its
+ * own calls and the block copies take); kv_pool 16-byte aligned.
  */
 typedef struct {
   int32_t num_blocks;
@@ -272,7 +280,8 @@ pa_status pa_prefill(void* out, const void* q, const void* kv_pool,
 
 /*
  * Block copy for copy-on-write: for i in [0, n) in order,
- *     kv_pool[dst[i]] = kv_pool[src[i]]    (the whole block: K and V, all heads).
+ *     kv_pool[dst[i]] = kv_pool[src[i]]    (the whole block: K and V, all heads,
+ * and an 8-bit pool's scales).
  * src, dst: device int32 [n]. Pairs must not overlap (no block is both a source
  * and a destination, no destination twice). An id outside [0, num_blocks)
  * skips that pair and sets PA_DEVERR_BLOCK. One call covers one layer's pool.
@@ -297,6 +306,153 @@ pa_status pa_copy_blocks(void* kv_pool, const int32_t* src, const int32_t* dst,
 pa_status pa_copy_blocks_between(void* dst_pool, int32_t dst_num_blocks, const void* src_pool,
                                  int32_t src_num_blocks, const int32_t* src, const int32_t* dst,
                                  int32_t n, pa_pool_desc pool, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit pools                                                                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * An 8-bit pool holds half the bytes of a bf16 one. It is one contiguous
+ * device buffer [num_blocks][pa_pool_block_bytes(pool)]; a block is
+ *     codes  [2][num_kv_heads][16][head_dim]  one byte each (K, then V)
+ *     scales [2][num_kv_heads]                fp32
+ * padded to a multiple of 128 bytes. An element is code * scale of its tile
+ * (block, K|V, kv head); pool.dtype says what a code is: PA_Q8_INT8 an int8 in
+ * [-127, 127], PA_Q8_E4M3 an e4m3 number. Slots, block tables and lengths are
+ * those of the other pools. pa_copy_blocks and pa_copy_blocks_between take
+ * 8-bit pools too and copy scales with the codes. k, v, q and out have a type
+ * of their own, io_dtype: PA_F32 or PA_BF16.
+ * Supported: block_size 16; head_dim 64 or 128; kv_pool 16-byte aligned.
+ */
+
+/* Bytes of one block of any pool (a multiple of 16; of 128 for 8-bit pools),
+ * 0 for an invalid descriptor. */
+int64_t pa_pool_block_bytes(pa_pool_desc pool);
+
+/*
+ * Cache append into an 8-bit pool: pa_reshape_and_cache with the rows coded on
+ * the way. For each tile that gains rows, with A the largest finite magnitude
+ * of its new rows (below 2^-100 counts as 0) and M = 127 (int8) or 448 (e4m3),
+ * all steps in fp32:
+ *   - its row 0 is among them: the tile starts afresh with scale A * (1/M), and
+ *     rows it is not given in this call hold no tokens any more;
+ *   - otherwise the scale s only grows. int8: max(s, A * (1/M)). e4m3: s if
+ *     A <= s * M, else s * 2^k with the smallest k that makes A / (s * M) <=
+ *     2^k (A * (1/M) where s is 0). Where it grew, all rows of the tile not
+ *     written now are coded again: code(value(c) * (s / s')).
+ *   - a new element x becomes the code nearest to x * (1/s'), ties to even.
+ * Error of an element, with s the tile's scale when it is read: int8 at most
+ * s/2 when the tile was written in one call, and at most s/2 more for each
+ * call that made s grow afterwards; e4m3 2^-4 relative (2^-10 * s absolute
+ * below the smallest normal), whether or not s grew.
+ * A NaN is stored as 0 and an infinity as the largest code of its sign (0 in a
+ * tile whose scale is 0), and either sets PA_DEVERR_NONFINITE.
+ * k, v: device, [num_tokens][num_kv_heads][head_dim] contiguous, io_dtype,
+ *       16-byte aligned.
+ * slot_mapping: as pa_reshape_and_cache. All tokens of one block must lie
+ *       within 32 consecutive entries (padding may lie between them), as a
+ *       sequence's tokens in order do; one that follows later than that, but
+ *       within 31 entries of the block's previous one, is not written and sets
+ *       PA_DEVERR_SLOT. A block that comes back after a longer gap would be
+ *       written by two warps at once: the caller must not do that (within 62
+ *       entries it sets PA_DEVERR_SLOT). Two tokens with the same slot (within
+ *       those 32 entries): the later one is stored.
+ */
+pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool,
+                                  const int64_t* slot_mapping, int32_t num_tokens,
+                                  pa_pool_desc pool, int32_t io_dtype, void* stream);
+
+/* Bytes of device workspace pa_decode_q8 needs; as pa_decode_workspace_size. */
+size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads,
+                                   pa_pool_desc pool, int32_t max_seq_len);
+
+/*
+ * pa_decode over an 8-bit pool: the same operation, arguments, checks and
+ * errors, with K_t and V_t = code * scale. q, out: io_dtype. Products are
+ * formed on the codes (exact in fp16) and accumulated in fp32; bf16 queries
+ * are exact too, probabilities are rounded to fp16 (2^-11 relative); fp32
+ * queries and their probabilities keep 22 bits.
+ */
+pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* seq_lens, int32_t num_seqs, int32_t num_heads,
+                       float scale, pa_pool_desc pool, int32_t io_dtype,
+                       void* workspace, size_t workspace_bytes,
+                       int32_t max_seq_len, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Tables of a step, built on the device                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The free blocks of a pool as a ring on the device: free_ring [ring_size]
+ * block ids, ring_state int32 {head, count, ...}: entries head .. head + count
+ * - 1 (modulo ring_size) are free, the head first ([C] §2.2 keeps the free
+ * blocks in a deque). A ring_size of num_blocks holds any state. The calls
+ * write int32 [4] {head, count, moved, refused}: `moved` the tokens granted
+ * (extend) or blocks given back (release), `refused` the requests that asked
+ * and got nothing. Blocks are taken and given back in request and table order,
+ * as pa_bm_allocate, pa_bm_append_slot and pa_bm_free do for one sequence after
+ * another, so tables and slots are the host block manager's. The requests own
+ * their blocks alone: the calls know no shared blocks (fork and copy-on-write
+ * stay with the host block manager).
+ * Each output may be the matching input (seq_lens_out = seq_lens,
+ * ring_state_out = ring_state); apart from that, outputs must not overlap
+ * inputs. All arrays are on the device. Nothing is allocated; the calls may be
+ * captured in a CUDA graph. workspace: device, 4-byte aligned,
+ * pa_tables_workspace_size(num_seqs) bytes, not used by another call at the
+ * same time. num_seqs at most 2^20.
+ */
+size_t pa_tables_workspace_size(int32_t num_seqs);
+
+/*
+ * Gives request b of length L = seq_lens[b] its n = new_tokens[b] next tokens:
+ * takes ceil((L + n) / 16) - ceil(L / 16) blocks from the ring's head, writes
+ * them to block_tables[b] from entry ceil(L / 16) on, and
+ *     seq_lens_out[b]   = L + n
+ *     query_start[b+1]  = query_start[b] + n,  query_start[0] = 0
+ *     slot_mapping      = the slot of each new token, -1 in every other entry.
+ * row_tokens 0: slot_mapping is packed, token i of request b at
+ * query_start[b] + i (the form of pa_prefill). row_tokens > 0: request b's
+ * tokens start at b * row_tokens (1: the form of pa_decode); num_slots must be
+ * at least num_seqs * row_tokens.
+ * A request gets all of its tokens or none. None (its length stays, query_start
+ * does not grow), and counted in `refused`:
+ *   - it needs blocks, and the blocks that it and the requests before it ask
+ *     for are more than the ring holds (later requests that need no block are
+ *     still served);
+ *   - packed, and its tokens and those of the requests before it are more than
+ *     num_slots;
+ *   - L < 0, n < 0, L + n > 16 * max_blocks_per_seq, or n > row_tokens > 0:
+ *     PA_DEVERR_SEQLEN is set too, and the request counts as asking for none.
+ * A block id outside [0, num_blocks), from the ring or in the table entry of a
+ * partial last block, gives slots of -1 and sets PA_DEVERR_BLOCK. A ring_state
+ * outside the ring sets PA_DEVERR_BLOCK, counts as an empty ring and is handed
+ * on as it is.
+ */
+pa_status pa_tables_extend(int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
+                           const int32_t* free_ring, int32_t ring_size, const int32_t* ring_state,
+                           int32_t num_blocks, int32_t* seq_lens_out, int32_t* query_start,
+                           int64_t* slot_mapping, int32_t num_slots, int32_t row_tokens,
+                           int32_t* ring_state_out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Gives the ceil(L / 16) blocks of every request with finished[b] != 0 back to
+ * the ring's tail and sets its length to 0 (its table row stays as it is); the
+ * other lengths are copied. A request whose blocks, with those of the finished
+ * requests before it, do not fit the ring keeps them and counts in `refused`,
+ * as does one with a length outside [0, 16 * max_blocks_per_seq], which sets
+ * PA_DEVERR_SEQLEN. An id outside [0, num_blocks) is put into the ring as it
+ * is and sets PA_DEVERR_BLOCK. A ring_state outside the ring sets
+ * PA_DEVERR_BLOCK, counts as a full ring and is handed on as it is.
+ */
+pa_status pa_tables_release(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* finished, int32_t num_seqs,
+                            int32_t* free_ring, int32_t ring_size, const int32_t* ring_state,
+                            int32_t num_blocks, int32_t* seq_lens_out, int32_t* ring_state_out,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error

@@ -10,6 +10,9 @@ Modules
   attention      fp64 gather-through-block-table + textbook softmax attention,
                  the split-KV partition/merge reading, the literal cache append
                  and block copy.
+  quantized      8-bit pools: codes and the append rule bit for bit, fp64
+                 attention over the values they stand for, error bounds.
+  tables         step tables (extend, release) one request after another.
   block_manager  integer block manager: FIFO free list, page tables, refcounts,
                  fork, copy-on-write of a shared partial last block, free.
   scheduler      integer continuous-batching step loop with recompute and

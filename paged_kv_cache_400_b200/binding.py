@@ -23,8 +23,9 @@ STATUS_NAMES = {
     0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "NO_BLOCKS",
     5: "UNKNOWN_SEQ", 6: "DEVICE_BOUNDS", 7: "SEQ_EXISTS", 8: "CAPACITY", 9: "WORKSPACE",
 }
-PA_F32, PA_BF16 = 0, 1
+PA_F32, PA_BF16, PA_Q8_INT8, PA_Q8_E4M3 = 0, 1, 2, 3
 PA_DEVERR_SLOT, PA_DEVERR_BLOCK, PA_DEVERR_SEQLEN, PA_DEVERR_TIMEOUT = 1, 2, 4, 8
+PA_DEVERR_NONFINITE = 16
 BLOCK_SIZE = 16
 
 
@@ -109,6 +110,13 @@ def _declare(lib):
         "pa_bm_num_cached": (i32, [vp]),
         "pa_prefill": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, f32, pa_pool_desc, i32, vp]),
         "pa_decode_noalloc": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, f32, pa_pool_desc, i32, vp]),
+        "pa_pool_block_bytes": (i64, [pa_pool_desc]),
+        "pa_reshape_and_cache_q8": (i32, [vp, vp, vp, vp, i32, pa_pool_desc, i32, vp]),
+        "pa_decode_q8_workspace_size": (sz, [i32, i32, pa_pool_desc, i32]),
+        "pa_decode_q8": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, f32, pa_pool_desc, i32, vp, sz, i32, vp]),
+        "pa_tables_workspace_size": (sz, [i32]),
+        "pa_tables_extend": (i32, [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
+        "pa_tables_release": (i32, [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -176,6 +184,8 @@ def _stream(stream):
 
 
 def pool_desc(kv_pool: torch.Tensor) -> pa_pool_desc:
+    if isinstance(kv_pool, Q8Pool):
+        raise ValueError("an 8-bit pool: this call takes fp32 and bf16 pools (the 8-bit calls end in _q8)")
     if kv_pool.dim() != 5 or kv_pool.shape[1] != 2 or kv_pool.shape[3] != BLOCK_SIZE:
         raise ValueError("kv_pool must be [num_blocks][2][num_kv_heads][16][head_dim]")
     dt = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}.get(kv_pool.dtype)
@@ -207,6 +217,8 @@ def pa_reshape_and_cache(k, v, kv_pool, slot_mapping, stream=None):
 
 
 def pa_decode_workspace_size(num_seqs, num_heads, kv_pool, max_seq_len) -> int:
+    if isinstance(kv_pool, Q8Pool):
+        return int(lib().pa_decode_q8_workspace_size(num_seqs, num_heads, kv_pool.desc, max_seq_len))
     desc = kv_pool if isinstance(kv_pool, pa_pool_desc) else pool_desc(kv_pool)
     return int(lib().pa_decode_workspace_size(num_seqs, num_heads, desc, max_seq_len))
 
@@ -217,7 +229,8 @@ def pa_decode_partition_tokens(num_seqs, num_heads, kv_pool, max_seq_len) -> int
 
 
 def alloc_workspace(num_seqs, num_heads, kv_pool, max_seq_len):
-    """Device workspace for pa_decode (None when none is needed)."""
+    """Device workspace for pa_decode, or for pa_decode_q8 over a Q8Pool (None
+    when none is needed)."""
     n = pa_decode_workspace_size(num_seqs, num_heads, kv_pool, max_seq_len)
     if n == 0:
         return None
@@ -306,7 +319,10 @@ def pa_decode_noalloc(out, q, kv_pool, block_tables, seq_lens, scale, max_seq_le
 
 
 def pa_copy_blocks(kv_pool, src, dst, stream=None):
-    desc = pool_desc(kv_pool)
+    if isinstance(kv_pool, Q8Pool):
+        desc, kv_pool = kv_pool.desc, kv_pool.buf
+    else:
+        desc = pool_desc(kv_pool)
     n = src.numel()
     if dst.numel() != n:
         raise ValueError("src and dst differ in length")
@@ -319,8 +335,17 @@ def pa_copy_blocks(kv_pool, src, dst, stream=None):
 
 def pa_copy_blocks_between(dst_pool, src_pool, src, dst, stream=None):
     """Block copy between two pools of one block shape (device or pinned host)."""
-    desc = pool_desc(dst_pool)
-    if pool_desc(src_pool).num_kv_heads != desc.num_kv_heads or src_pool.shape[1:] != dst_pool.shape[1:] \
+    if isinstance(dst_pool, Q8Pool) != isinstance(src_pool, Q8Pool):
+        raise ValueError("pools differ in block shape")
+    if isinstance(dst_pool, Q8Pool):
+        desc = dst_pool.desc
+        if (src_pool.num_kv_heads, src_pool.head_dim, src_pool.code) != (dst_pool.num_kv_heads, dst_pool.head_dim,
+                                                                         dst_pool.code):
+            raise ValueError("pools differ in block shape")
+        dst_pool, src_pool = dst_pool.buf, src_pool.buf
+    else:
+        desc = pool_desc(dst_pool)
+    if dst_pool.dim() == 5 and pool_desc(src_pool).num_kv_heads != desc.num_kv_heads or src_pool.shape[1:] != dst_pool.shape[1:] \
             or src_pool.dtype != dst_pool.dtype:
         raise ValueError("pools differ in block shape")
     n = src.numel()
@@ -338,6 +363,187 @@ def pa_copy_blocks_between(dst_pool, src_pool, src, dst, stream=None):
     _check("pa_copy_blocks_between", lib().pa_copy_blocks_between(
         C.c_void_p(dst_pool.data_ptr()), dst_pool.shape[0], C.c_void_p(src_pool.data_ptr()), src_pool.shape[0],
         C.c_void_p(src.data_ptr()), C.c_void_p(dst.data_ptr()), n, desc, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit pools
+# ---------------------------------------------------------------------------
+class Q8Pool:
+    """KV pool of one attention layer in 8 bits: one uint8 buffer
+    [num_blocks][block_bytes] (`buf`), a block's codes [2][num_kv_heads][16]
+    [head_dim] and fp32 scales [2][num_kv_heads] with padding behind them. An
+    element is code * scale of its (block, K|V, head) tile; `code` is "int8" or
+    "e4m3". `codes` and `scales` are views of the buffer."""
+
+    _CODES = {"int8": (PA_Q8_INT8, torch.int8), "e4m3": (PA_Q8_E4M3, torch.float8_e4m3fn)}
+
+    def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, code: str = "int8", device="cuda"):
+        n = self.block_bytes(num_kv_heads, head_dim, code)
+        self._set(torch.zeros(num_blocks, n, dtype=torch.uint8, device=device), num_kv_heads, head_dim, code)
+
+    @classmethod
+    def wrap(cls, buf: torch.Tensor, num_kv_heads: int, head_dim: int, code: str = "int8") -> "Q8Pool":
+        """A pool over an existing uint8 buffer [num_blocks][block_bytes] on the
+        device, or in pinned host memory for pa_copy_blocks_between."""
+        self = cls.__new__(cls)
+        self._set(buf, num_kv_heads, head_dim, code)
+        return self
+
+    @classmethod
+    def block_bytes(cls, num_kv_heads: int, head_dim: int, code: str = "int8") -> int:
+        if code not in cls._CODES:
+            raise ValueError(f"code {code!r} (one of {sorted(cls._CODES)})")
+        n = int(lib().pa_pool_block_bytes(pa_pool_desc(1, num_kv_heads, head_dim, BLOCK_SIZE, cls._CODES[code][0])))
+        if n == 0:
+            raise ValueError(f"no 8-bit pool with {num_kv_heads} KV heads of head_dim {head_dim}")
+        return n
+
+    def _set(self, buf, num_kv_heads, head_dim, code):
+        n = self.block_bytes(num_kv_heads, head_dim, code)
+        if buf.dim() != 2 or buf.shape[1] != n or buf.dtype != torch.uint8 or not buf.is_contiguous():
+            raise ValueError(f"buf must be contiguous uint8 [num_blocks][{n}]")
+        self.buf, self.num_kv_heads, self.head_dim, self.code = buf, num_kv_heads, head_dim, code
+        self.num_blocks = buf.shape[0]
+        self.desc = pa_pool_desc(buf.shape[0], num_kv_heads, head_dim, BLOCK_SIZE, self._CODES[code][0])
+
+    @property
+    def device(self):
+        return self.buf.device
+
+    @property
+    def codes(self) -> torch.Tensor:
+        """[num_blocks][2][num_kv_heads][16][head_dim], int8 or float8_e4m3fn."""
+        raw = 2 * self.num_kv_heads * BLOCK_SIZE * self.head_dim
+        return self.buf[:, :raw].view(self._CODES[self.code][1]).unflatten(
+            1, (2, self.num_kv_heads, BLOCK_SIZE, self.head_dim))
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """[num_blocks][2][num_kv_heads] fp32."""
+        raw = 2 * self.num_kv_heads * BLOCK_SIZE * self.head_dim
+        return self.buf[:, raw:raw + 8 * self.num_kv_heads].view(torch.float32).unflatten(1, (2, self.num_kv_heads))
+
+
+def _here(t: torch.Tensor, name: str, *dtypes) -> C.c_void_p:
+    """As _dev, for a tensor that must lie on the current device (the library
+    launches there) and have one of `dtypes`."""
+    p = _dev(t, name)
+    if dtypes and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return p
+
+
+_IO = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
+
+
+def _q8_pool(pool) -> Q8Pool:
+    if not isinstance(pool, Q8Pool):
+        raise ValueError("pool must be a Q8Pool")
+    return pool
+
+
+def pa_reshape_and_cache_q8(k, v, pool, slot_mapping, stream=None):
+    """Codes the rows k, v [num_tokens][num_kv_heads][head_dim] (fp32 or bf16)
+    into their slots of a Q8Pool. All tokens of one block lie within 32
+    consecutive entries of slot_mapping."""
+    pool = _q8_pool(pool)
+    n = slot_mapping.numel()
+    if k.shape != (n, pool.num_kv_heads, pool.head_dim) or v.shape != k.shape:
+        raise ValueError("k, v must be [num_tokens][num_kv_heads][head_dim]")
+    if n == 0:
+        return
+    _check("pa_reshape_and_cache_q8", lib().pa_reshape_and_cache_q8(
+        _here(k, "k", *_IO), _here(v, "v", k.dtype), _here(pool.buf, "pool"),
+        _here(slot_mapping, "slot_mapping", torch.int64), n, pool.desc, _IO[k.dtype], _stream(stream)))
+
+
+def pa_decode_q8(out, q, pool, block_tables, seq_lens, scale, max_seq_len, workspace=None, stream=None):
+    """pa_decode over a Q8Pool; q, out [num_seqs][num_heads][head_dim], fp32 or
+    bf16; workspace: alloc_workspace(num_seqs, num_heads, pool, max_seq_len)."""
+    pool = _q8_pool(pool)
+    B, H, D = q.shape
+    if out.shape != q.shape or D != pool.head_dim:
+        raise ValueError("q, out must be [num_seqs][num_heads][head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], seq_lens [num_seqs]")
+    ws_ptr, ws_bytes = C.c_void_p(0), 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _here(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _check("pa_decode_q8", lib().pa_decode_q8(
+        _here(out, "out", q.dtype), _here(q, "q", *_IO), _here(pool.buf, "pool"),
+        _here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+        _here(seq_lens, "seq_lens", torch.int32), B, H, float(scale), pool.desc, _IO[q.dtype], ws_ptr, ws_bytes,
+        int(max_seq_len), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# tables of a step, built on the device
+# ---------------------------------------------------------------------------
+def alloc_tables_workspace(num_seqs: int, device="cuda") -> torch.Tensor:
+    """Device workspace for pa_tables_extend and pa_tables_release."""
+    n = int(lib().pa_tables_workspace_size(int(num_seqs)))
+    if n == 0:
+        raise ValueError(f"num_seqs {num_seqs} not supported")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def make_free_ring(num_blocks: int, order=None, device="cuda"):
+    """(free_ring, ring_state) of a pool whose blocks are all free, handed out
+    in `order` (0, 1, ... by default)."""
+    ring = torch.arange(num_blocks, dtype=torch.int32) if order is None else torch.as_tensor(order, dtype=torch.int32)
+    if ring.shape != (num_blocks,):
+        raise ValueError("order must name every block once")
+    return ring.to(device), torch.tensor([0, num_blocks, 0, 0], dtype=torch.int32, device=device)
+
+
+def _tables_args(block_tables, seq_lens, asked, name, seq_lens_out, ring_state, ring_state_out):
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if B < 0 or block_tables.dim() != 2 or block_tables.shape[0] != B or asked.shape != (B,) \
+            or seq_lens_out.shape != (B,):
+        raise ValueError(f"block_tables [num_seqs][max_blocks]; seq_lens, {name}, seq_lens_out [num_seqs]")
+    if ring_state.numel() < 2 or ring_state_out.shape != (4,):
+        raise ValueError("ring_state holds head and count, ring_state_out [4]")
+    return B
+
+
+def pa_tables_extend(block_tables, seq_lens, new_tokens, free_ring, ring_state, seq_lens_out, query_start,
+                     slot_mapping, ring_state_out, num_blocks, row_tokens=0, workspace=None, stream=None):
+    """Gives each request its new_tokens next tokens: takes their blocks from
+    the free ring, extends block_tables in place, and writes the new lengths,
+    query_start and the tokens' slots (packed, or row_tokens per request)."""
+    B = _tables_args(block_tables, seq_lens, new_tokens, "new_tokens", seq_lens_out, ring_state, ring_state_out)
+    if query_start.shape != (B + 1,) or slot_mapping.dim() != 1 or free_ring.dim() != 1:
+        raise ValueError("query_start [num_seqs + 1], slot_mapping [num_slots], free_ring [ring_size]")
+    if workspace is None:
+        workspace = alloc_tables_workspace(B, seq_lens.device)
+    i = torch.int32
+    _check("pa_tables_extend", lib().pa_tables_extend(
+        _here(block_tables, "block_tables", i), block_tables.shape[1], _here(seq_lens, "seq_lens", i),
+        _here(new_tokens, "new_tokens", i), B, _here(free_ring, "free_ring", i), free_ring.numel(),
+        _here(ring_state, "ring_state", i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", i),
+        _here(query_start, "query_start", i), _here(slot_mapping, "slot_mapping", torch.int64),
+        slot_mapping.numel(), int(row_tokens), _here(ring_state_out, "ring_state_out", i),
+        _here(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pa_tables_release(block_tables, seq_lens, finished, free_ring, ring_state, seq_lens_out, ring_state_out,
+                      num_blocks, workspace=None, stream=None):
+    """Gives the blocks of every request with finished[b] != 0 back to the free
+    ring (in place) and sets its length to 0."""
+    B = _tables_args(block_tables, seq_lens, finished, "finished", seq_lens_out, ring_state, ring_state_out)
+    if free_ring.dim() != 1:
+        raise ValueError("free_ring [ring_size]")
+    if workspace is None:
+        workspace = alloc_tables_workspace(B, seq_lens.device)
+    i = torch.int32
+    _check("pa_tables_release", lib().pa_tables_release(
+        _here(block_tables, "block_tables", i), block_tables.shape[1], _here(seq_lens, "seq_lens", i),
+        _here(finished, "finished", i), B, _here(free_ring, "free_ring", i), free_ring.numel(),
+        _here(ring_state, "ring_state", i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", i),
+        _here(ring_state_out, "ring_state_out", i), _here(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def pa_selftest_timeout(limit_ns: int, stream=None):

@@ -527,6 +527,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxPartitionBlocks = 128;  // partitions of at most 2048 tokens
 static_assert(kMaxPartitionBlocks <= 4 * 32, "the plan's scan covers 4 sizes per lane of one warp");
 
+// kRowChunks: 16-byte chunks of one head's output row.
+template <int32_t kRowChunks>
 __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(DecodeParams p) {
   __shared__ int32_t cnt[kMaxPartitionBlocks + 1];
   __shared__ int32_t off[kMaxPartitionBlocks + 1];
@@ -540,8 +542,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(DecodeParams 
   for (int32_t b = threadIdx.x; b < p.num_seqs; b += blockDim.x) {
     const int32_t L = checked_len(p, b, true);
     if (L == 0) {
-      uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t)b * p.num_heads * 128);
-      for (int32_t i = 0; i < p.num_heads * 16; ++i) o[i] = make_uint4(0, 0, 0, 0);
+      uint4* o = reinterpret_cast<uint4*>(p.out) + (size_t)b * p.num_heads * kRowChunks;
+      for (int32_t i = 0; i < p.num_heads * kRowChunks; ++i) o[i] = make_uint4(0, 0, 0, 0);
       continue;
     }
     const int32_t n = (L + p.partition_tokens - 1) / p.partition_tokens;
@@ -679,7 +681,7 @@ inline pa_status launch_staged_bf16_d128(const DecodeParams& p, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, decode_plan_kernel, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, decode_plan_kernel<16>, p);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode (plan): launch failed: %s", cudaGetErrorString(e));
   }
   const bool append = p.k_new != nullptr;

@@ -7,11 +7,14 @@
 
 #include "../host/errors.hpp"
 #include "append.cuh"
+#include "append_q8.cuh"
 #include "common.cuh"
 #include "decode_common.cuh"
 #include "decode_generic.cuh"
+#include "decode_q8.cuh"
 #include "decode_staged.cuh"
 #include "prefill_tc.cuh"
+#include "tables.cuh"
 #ifdef PA_PREFILL_MMA_SYNC
 #include "prefill.cuh"  // comparison build only: the mma.sync prefill kernel
 #endif
@@ -34,10 +37,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t elem_size(int32_t dtype) { return dtype == PA_BF16 ? 2 : 4; }
 
-pa_status check_pool(const pa_pool_desc& pool, const char* fn) {
+bool is_q8(int32_t dtype) { return dtype == PA_Q8_INT8 || dtype == PA_Q8_E4M3; }
+
+// Element types a call takes in its pool.
+enum class PoolTypes { kWide, kQ8, kAny };
+
+pa_status check_pool(const pa_pool_desc& pool, const char* fn, PoolTypes types = PoolTypes::kWide) {
   if (pool.block_size != PA_BLOCK_SIZE)
     return fail(PA_ERR_UNSUPPORTED, "%s: block_size %d (only 16)", fn, pool.block_size);
-  if (pool.dtype != PA_F32 && pool.dtype != PA_BF16)
+  const bool wide = pool.dtype == PA_F32 || pool.dtype == PA_BF16;
+  if (!(wide && types != PoolTypes::kQ8) && !(is_q8(pool.dtype) && types != PoolTypes::kWide))
     return fail(PA_ERR_UNSUPPORTED, "%s: dtype %d", fn, pool.dtype);
   if (pool.head_dim != 64 && pool.head_dim != 128)
     return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d (64 or 128)", fn, pool.head_dim);
@@ -45,6 +54,12 @@ pa_status check_pool(const pa_pool_desc& pool, const char* fn) {
     return fail(PA_ERR_INVALID_ARG, "%s: num_blocks %d, num_kv_heads %d", fn, pool.num_blocks,
                 pool.num_kv_heads);
   return PA_OK;
+}
+
+// Bytes of one block, an 8-bit pool's scales included; a multiple of 16.
+int64_t block_bytes_of(const pa_pool_desc& pool) {
+  if (is_q8(pool.dtype)) return pagedkv::q8_layout(pool.num_kv_heads, pool.head_dim).block_bytes;
+  return (int64_t)2 * pool.num_kv_heads * PA_BLOCK_SIZE * pool.head_dim * (int64_t)elem_size(pool.dtype);
 }
 
 pa_status launch_status(const char* fn) {
@@ -74,15 +89,15 @@ int32_t partition_tokens_for(int32_t num_seqs, const pa_pool_desc& pool, int32_t
 // The persistent decode's work items hold the partition index in 16 bits.
 constexpr int64_t kMaxPartitions = 65535;
 
-// Host-side checks shared by pa_decode, pa_append_decode and
-// pa_decode_noalloc, in this order: pool, sizes, head group, table width,
+// Host-side checks shared by pa_decode, pa_append_decode, pa_decode_noalloc
+// and pa_decode_q8, in this order: pool, sizes, head group, table width,
 // scale, then (for a non-empty batch) the partition count, pointers and
 // alignment. The workspace is checked by the caller afterwards.
 pa_status check_decode_args(const char* fn, const void* out, const void* q, const void* kv_pool,
                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
                             int32_t num_seqs, int32_t num_heads, float scale, const pa_pool_desc& pool,
-                            int32_t max_seq_len) {
-  pa_status s = check_pool(pool, fn);
+                            int32_t max_seq_len, PoolTypes types = PoolTypes::kWide) {
+  pa_status s = check_pool(pool, fn, types);
   if (s != PA_OK) return s;
   if (num_seqs < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0)
     return fail(PA_ERR_INVALID_ARG, "%s: num_seqs %d, num_heads %d, max_blocks %d, max_seq_len %d", fn, num_seqs,
@@ -378,14 +393,13 @@ pa_status pa_prefill(void* out, const void* q, const void* kv_pool, const int32_
 
 pa_status pa_copy_blocks(void* kv_pool, const int32_t* src, const int32_t* dst, int32_t n,
                          pa_pool_desc pool, void* stream) {
-  pa_status s = check_pool(pool, "pa_copy_blocks");
+  pa_status s = check_pool(pool, "pa_copy_blocks", PoolTypes::kAny);
   if (s != PA_OK) return s;
   if (n < 0) return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks: n %d", n);
   if (n == 0) return PA_OK;
   if (!kv_pool || !src || !dst) return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks: NULL pointer");
   if (!aligned16(kv_pool)) return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks: kv_pool must be 16-byte aligned");
-  const int64_t chunks = (int64_t)2 * pool.num_kv_heads * PA_BLOCK_SIZE * pool.head_dim *
-                         (int64_t)elem_size(pool.dtype) / 16;
+  const int64_t chunks = block_bytes_of(pool) / 16;
   pagedkv::copy_blocks_kernel<<<n, 256, 0, (cudaStream_t)stream>>>(
       reinterpret_cast<uint4*>(kv_pool), src, dst, pool.num_blocks, chunks);
   return launch_status("pa_copy_blocks");
@@ -419,7 +433,7 @@ pa_status pa_copy_blocks_between(void* dst_pool, int32_t dst_num_blocks, const v
                                  pa_pool_desc pool, void* stream) {
   pa_pool_desc d = pool;
   d.num_blocks = 1;
-  pa_status s = check_pool(d, "pa_copy_blocks_between");
+  pa_status s = check_pool(d, "pa_copy_blocks_between", PoolTypes::kAny);
   if (s != PA_OK) return s;
   if (n < 0 || dst_num_blocks <= 0 || src_num_blocks <= 0)
     return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks_between: n %d, blocks %d / %d", n, dst_num_blocks,
@@ -429,8 +443,7 @@ pa_status pa_copy_blocks_between(void* dst_pool, int32_t dst_num_blocks, const v
     return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks_between: NULL pointer");
   if (!aligned16(dst_pool) || !aligned16(src_pool))
     return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks_between: pools must be 16-byte aligned");
-  const size_t block_bytes =
-      (size_t)2 * pool.num_kv_heads * PA_BLOCK_SIZE * pool.head_dim * elem_size(pool.dtype);
+  const size_t block_bytes = (size_t)block_bytes_of(pool);
   if ((s = check_addressable(dst_pool, block_bytes * dst_num_blocks, "pa_copy_blocks_between", "dst_pool")) != PA_OK)
     return s;
   if ((s = check_addressable(src_pool, block_bytes * src_num_blocks, "pa_copy_blocks_between", "src_pool")) != PA_OK)
@@ -481,6 +494,200 @@ pa_status pa_get_device_error(uint32_t* flags, void* stream) {
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_get_device_error: %s", cudaGetErrorString(e));
   *flags = v;
   return v ? PA_ERR_DEVICE_BOUNDS : PA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 8-bit pools
+// ---------------------------------------------------------------------------
+extern "C" {
+
+int64_t pa_pool_block_bytes(pa_pool_desc pool) {
+  if (check_pool(pool, "pa_pool_block_bytes", PoolTypes::kAny) != PA_OK) return 0;
+  return block_bytes_of(pool);
+}
+
+pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool, const int64_t* slot_mapping,
+                                  int32_t num_tokens, pa_pool_desc pool, int32_t io_dtype, void* stream) {
+  const char* fn = "pa_reshape_and_cache_q8";
+  pa_status s = check_pool(pool, fn, PoolTypes::kQ8);
+  if (s != PA_OK) return s;
+  if (io_dtype != PA_F32 && io_dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "%s: io_dtype %d", fn, io_dtype);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "%s: num_tokens %d", fn, num_tokens);
+  if (pool.num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 65535", fn, pool.num_kv_heads);
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !kv_pool || !slot_mapping) return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kv_pool))
+    return fail(PA_ERR_INVALID_ARG, "%s: k, v and kv_pool must be 16-byte aligned", fn);
+  cudaStream_t st = (cudaStream_t)stream;
+  auto run = [&](auto io, auto code) {
+    using T = decltype(io);
+    using Code = decltype(code);
+    return pool.head_dim == 128
+               ? pagedkv::launch_append_q8<T, 128, Code>(k, v, kv_pool, slot_mapping, num_tokens, pool.num_kv_heads,
+                                                         pool.num_blocks, st)
+               : pagedkv::launch_append_q8<T, 64, Code>(k, v, kv_pool, slot_mapping, num_tokens, pool.num_kv_heads,
+                                                        pool.num_blocks, st);
+  };
+  auto run_io = [&](auto code) { return io_dtype == PA_BF16 ? run(__nv_bfloat16{}, code) : run(float{}, code); };
+  const cudaError_t e =
+      pool.dtype == PA_Q8_INT8 ? run_io(pagedkv::CodeInt8{}) : run_io(pagedkv::CodeE4m3{});
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return PA_OK;
+}
+
+size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads, pa_pool_desc pool, int32_t max_seq_len) {
+  return pa_decode_workspace_size(num_seqs, num_heads, pool, max_seq_len);
+}
+
+pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int32_t* block_tables,
+                       int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, int32_t num_heads,
+                       float scale, pa_pool_desc pool, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                       int32_t max_seq_len, void* stream) {
+  const char* fn = "pa_decode_q8";
+  if (io_dtype != PA_F32 && io_dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "%s: io_dtype %d", fn, io_dtype);
+  pa_status s = check_decode_args(fn, out, q, kv_pool, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                  num_heads, scale, pool, max_seq_len, PoolTypes::kQ8);
+  if (s != PA_OK) return s;
+  if (pool.num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 65535", fn, pool.num_kv_heads);
+  if (num_seqs == 0) return PA_OK;
+  const int32_t len = max_seq_len > 0 ? max_seq_len : 1;
+  const WorkspaceLayout w = workspace_layout(num_seqs, num_heads, pool, len);
+  if (w.total > 0 && (!workspace || workspace_bytes < w.total))
+    return fail(PA_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", fn, workspace_bytes, workspace, w.total);
+  if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  char* ws = reinterpret_cast<char*>(workspace);
+  const bool use_list = w.total && w.partitions >= kWorkListPartitions;
+  pagedkv::DecodeParams p = {};
+  p.out = out;
+  p.q = q;
+  p.pool = kv_pool;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.ws_acc = reinterpret_cast<float*>(ws);
+  p.ws_ml = w.total ? reinterpret_cast<float*>(ws + w.ml_offset) : nullptr;
+  p.work_items = use_list ? reinterpret_cast<int32_t*>(ws + w.items_offset) : nullptr;
+  p.work_header = use_list ? reinterpret_cast<int32_t*>(ws + w.header_offset) : nullptr;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = pool.num_kv_heads;
+  p.group = num_heads / pool.num_kv_heads;
+  p.num_blocks = pool.num_blocks;
+  p.max_seq_len = max_seq_len;
+  p.partition_tokens = partition_tokens_for(num_seqs, pool, len);
+  p.max_partitions = w.partitions > 0 ? w.partitions : 1;
+  p.scale_log2 = scale * pagedkv::kLog2e;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (io_dtype == PA_BF16)
+    return pool.head_dim == 128 ? pagedkv::launch_decode_q8_code<__nv_bfloat16, 128>(p, pool.dtype, st)
+                                : pagedkv::launch_decode_q8_code<__nv_bfloat16, 64>(p, pool.dtype, st);
+  return pool.head_dim == 128 ? pagedkv::launch_decode_q8_code<float, 128>(p, pool.dtype, st)
+                              : pagedkv::launch_decode_q8_code<float, 64>(p, pool.dtype, st);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// tables built on the device
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int32_t kTablesMaxSeqs = 1 << 20;
+
+pa_status check_tables(const char* fn, const void* tables, const void* lens, const void* asked, const void* ring,
+                       const void* state, const void* lens_out, const void* state_out, int32_t num_seqs,
+                       int32_t max_blocks_per_seq, int32_t ring_size, int32_t num_blocks, const void* workspace,
+                       size_t workspace_bytes) {
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || ring_size <= 0 || num_blocks <= 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: num_seqs %d, max_blocks %d, ring_size %d, num_blocks %d", fn, num_seqs,
+                max_blocks_per_seq, ring_size, num_blocks);
+  if (num_seqs > kTablesMaxSeqs) return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs %d > %d", fn, num_seqs, kTablesMaxSeqs);
+  if ((int64_t)max_blocks_per_seq * PA_BLOCK_SIZE > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: max_blocks %d * 16 tokens pass 32 bits", fn, max_blocks_per_seq);
+  if (!ring || !state || !state_out || (num_seqs > 0 && (!tables || !lens || !asked || !lens_out)))
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!workspace || workspace_bytes < pagedkv::tables_workspace_bytes(num_seqs))
+    return fail(PA_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", fn, workspace_bytes, workspace,
+                pagedkv::tables_workspace_bytes(num_seqs));
+  if (reinterpret_cast<uintptr_t>(workspace) & 3u)
+    return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 4-byte aligned", fn);
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_tables_workspace_size(int32_t num_seqs) {
+  return num_seqs < 0 || num_seqs > kTablesMaxSeqs ? 0 : pagedkv::tables_workspace_bytes(num_seqs);
+}
+
+pa_status pa_tables_extend(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* new_tokens, int32_t num_seqs, const int32_t* free_ring, int32_t ring_size,
+                           const int32_t* ring_state, int32_t num_blocks, int32_t* seq_lens_out,
+                           int32_t* query_start, int64_t* slot_mapping, int32_t num_slots, int32_t row_tokens,
+                           int32_t* ring_state_out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "pa_tables_extend";
+  pa_status s = check_tables(fn, block_tables, seq_lens, new_tokens, free_ring, ring_state, seq_lens_out,
+                             ring_state_out, num_seqs, max_blocks_per_seq, ring_size, num_blocks, workspace,
+                             workspace_bytes);
+  if (s != PA_OK) return s;
+  if (num_slots < 0 || row_tokens < 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: num_slots %d, row_tokens %d", fn, num_slots, row_tokens);
+  if (row_tokens > 0 && (int64_t)num_seqs * row_tokens > num_slots)
+    return fail(PA_ERR_INVALID_ARG, "%s: num_slots %d < num_seqs * row_tokens", fn, num_slots);
+  if (!query_start || (num_slots > 0 && !slot_mapping)) return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  pagedkv::TablesParams t = {};
+  t.block_tables = block_tables;
+  t.seq_lens = seq_lens;
+  t.asked = new_tokens;
+  t.ring = const_cast<int32_t*>(free_ring);  // only read
+  t.state = ring_state;
+  t.lens_out = seq_lens_out;
+  t.query_start = query_start;
+  t.slots = slot_mapping;
+  t.state_out = ring_state_out;
+  t.num_seqs = num_seqs;
+  t.width = max_blocks_per_seq;
+  t.ring_size = ring_size;
+  t.num_blocks = num_blocks;
+  t.num_slots = num_slots;
+  t.row_tokens = row_tokens;
+  const cudaError_t e = pagedkv::launch_tables<true>(t, workspace, num_slots, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return PA_OK;
+}
+
+pa_status pa_tables_release(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                            const int32_t* finished, int32_t num_seqs, int32_t* free_ring, int32_t ring_size,
+                            const int32_t* ring_state, int32_t num_blocks, int32_t* seq_lens_out,
+                            int32_t* ring_state_out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "pa_tables_release";
+  pa_status s = check_tables(fn, block_tables, seq_lens, finished, free_ring, ring_state, seq_lens_out,
+                             ring_state_out, num_seqs, max_blocks_per_seq, ring_size, num_blocks, workspace,
+                             workspace_bytes);
+  if (s != PA_OK) return s;
+  pagedkv::TablesParams t = {};
+  t.block_tables = const_cast<int32_t*>(block_tables);  // only read
+  t.seq_lens = seq_lens;
+  t.asked = finished;
+  t.ring = free_ring;
+  t.state = ring_state;
+  t.lens_out = seq_lens_out;
+  t.state_out = ring_state_out;
+  t.num_seqs = num_seqs;
+  t.width = max_blocks_per_seq;
+  t.ring_size = ring_size;
+  t.num_blocks = num_blocks;
+  const int64_t most = std::min<int64_t>(ring_size, (int64_t)num_seqs * max_blocks_per_seq);
+  const cudaError_t e = pagedkv::launch_tables<false>(t, workspace, most, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return PA_OK;
 }
 
 }  // extern "C"
