@@ -380,6 +380,20 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
                        void* workspace, size_t workspace_bytes,
                        int32_t max_seq_len, void* stream);
 
+/*
+ * pa_prefill over an 8-bit pool: the same operation, arguments, checks and
+ * errors, with K_t and V_t = code * scale; q, out bf16. Products are formed on
+ * the codes (exact in bf16) and accumulated in fp32; a probability times its
+ * V scale is rounded to bf16 (2^-8 relative), as pa_prefill rounds its
+ * probabilities. Supported: head_dim 128, num_heads / num_kv_heads in
+ * {1, 2, 4, 8, 16}, scale >= 0 (else PA_ERR_INVALID_ARG).
+ */
+pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* seq_lens, const int32_t* query_start,
+                        int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale,
+                        pa_pool_desc pool, int32_t max_query_len, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Tables of a step, built on the device                                      */
 /* ------------------------------------------------------------------------ */

@@ -114,6 +114,7 @@ def _declare(lib):
         "pa_reshape_and_cache_q8": (i32, [vp, vp, vp, vp, i32, pa_pool_desc, i32, vp]),
         "pa_decode_q8_workspace_size": (sz, [i32, i32, pa_pool_desc, i32]),
         "pa_decode_q8": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, f32, pa_pool_desc, i32, vp, sz, i32, vp]),
+        "pa_prefill_q8": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, f32, pa_pool_desc, i32, vp]),
         "pa_tables_workspace_size": (sz, [i32]),
         "pa_tables_extend": (i32, [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
         "pa_tables_release": (i32, [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, sz, vp]),
@@ -476,6 +477,24 @@ def pa_decode_q8(out, q, pool, block_tables, seq_lens, scale, max_seq_len, works
         _here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
         _here(seq_lens, "seq_lens", torch.int32), B, H, float(scale), pool.desc, _IO[q.dtype], ws_ptr, ws_bytes,
         int(max_seq_len), _stream(stream)))
+
+
+def pa_prefill_q8(out, q, pool, block_tables, seq_lens, query_start, scale, max_query_len, stream=None):
+    """pa_prefill over a Q8Pool of head_dim 128; q, out [total new tokens]
+    [num_heads][128] bf16."""
+    pool = _q8_pool(pool)
+    T, H, D = q.shape
+    B = seq_lens.shape[0]
+    if out.shape != q.shape or D != pool.head_dim:
+        raise ValueError("q, out must be [num_tokens][num_heads][head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,) \
+            or query_start.shape != (B + 1,):
+        raise ValueError("block_tables [num_seqs][max_blocks], seq_lens [num_seqs], query_start [num_seqs+1]")
+    _check("pa_prefill_q8", lib().pa_prefill_q8(
+        _here(out, "out", torch.bfloat16), _here(q, "q", torch.bfloat16), _here(pool.buf, "pool"),
+        _here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+        _here(seq_lens, "seq_lens", torch.int32), _here(query_start, "query_start", torch.int32), B, T, H,
+        float(scale), pool.desc, int(max_query_len), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

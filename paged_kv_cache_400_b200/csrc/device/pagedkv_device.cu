@@ -122,6 +122,37 @@ pa_status check_decode_args(const char* fn, const void* out, const void* q, cons
   return PA_OK;
 }
 
+// Host-side checks shared by pa_prefill and pa_prefill_q8, after the pool's.
+pa_status check_prefill_args(const char* fn, const void* out, const void* q, const void* kv_pool,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                             const int32_t* query_start, int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                             float scale, const pa_pool_desc& pool, int32_t max_query_len) {
+  if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_query_len < 0)
+    return fail(PA_ERR_INVALID_ARG,
+                "%s: num_seqs %d, num_tokens %d, num_heads %d, max_blocks %d, max_query_len %d", fn, num_seqs,
+                num_tokens, num_heads, max_blocks_per_seq, max_query_len);
+  if (max_query_len > num_tokens)
+    return fail(PA_ERR_INVALID_ARG, "%s: max_query_len %d > num_tokens %d", fn, max_query_len, num_tokens);
+  if (num_heads % pool.num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: num_heads %d not a multiple of num_kv_heads %d", fn, num_heads,
+                pool.num_kv_heads);
+  const int32_t G = num_heads / pool.num_kv_heads;
+  if (G > 16 || (G & (G - 1)) != 0)
+    return fail(PA_ERR_UNSUPPORTED, "%s: head group %d (1, 2, 4, 8 or 16)", fn, G);
+  if (num_seqs > 65535 || pool.num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs %d or num_kv_heads %d > 65535", fn, num_seqs,
+                pool.num_kv_heads);
+  if ((int64_t)max_query_len > (int64_t)max_blocks_per_seq * PA_BLOCK_SIZE)
+    return fail(PA_ERR_INVALID_ARG, "%s: max_query_len %d > max_blocks_per_seq * 16", fn, max_query_len);
+  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  if (num_seqs == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !q || !kv_pool || !block_tables || !seq_lens || !query_start)
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_pool))
+    return fail(PA_ERR_INVALID_ARG, "%s: out, q and kv_pool must be 16-byte aligned", fn);
+  return PA_OK;
+}
+
 struct WorkspaceLayout {
   size_t acc_bytes, ml_offset, items_offset, header_offset, total;
   int32_t partitions;
@@ -343,29 +374,9 @@ pa_status pa_prefill(void* out, const void* q, const void* kv_pool, const int32_
   if (s != PA_OK) return s;
   if (pool.dtype != PA_BF16 || pool.head_dim != 128)
     return fail(PA_ERR_UNSUPPORTED, "pa_prefill: only bf16 pools with head_dim 128");
-  if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_query_len < 0)
-    return fail(PA_ERR_INVALID_ARG,
-                "pa_prefill: num_seqs %d, num_tokens %d, num_heads %d, max_blocks %d, max_query_len %d", num_seqs,
-                num_tokens, num_heads, max_blocks_per_seq, max_query_len);
-  if (max_query_len > num_tokens)
-    return fail(PA_ERR_INVALID_ARG, "pa_prefill: max_query_len %d > num_tokens %d", max_query_len, num_tokens);
-  if (num_heads % pool.num_kv_heads != 0)
-    return fail(PA_ERR_INVALID_ARG, "pa_prefill: num_heads %d not a multiple of num_kv_heads %d", num_heads,
-                pool.num_kv_heads);
-  const int32_t G = num_heads / pool.num_kv_heads;
-  if (G > 16 || (G & (G - 1)) != 0)
-    return fail(PA_ERR_UNSUPPORTED, "pa_prefill: head group %d (1, 2, 4, 8 or 16)", G);
-  if (num_seqs > 65535 || pool.num_kv_heads > 65535)
-    return fail(PA_ERR_UNSUPPORTED, "pa_prefill: num_seqs %d or num_kv_heads %d > 65535", num_seqs,
-                pool.num_kv_heads);
-  if ((int64_t)max_query_len > (int64_t)max_blocks_per_seq * PA_BLOCK_SIZE)
-    return fail(PA_ERR_INVALID_ARG, "pa_prefill: max_query_len %d > max_blocks_per_seq * 16", max_query_len);
-  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "pa_prefill: scale is not finite");
-  if (num_seqs == 0 || max_query_len == 0) return PA_OK;
-  if (!out || !q || !kv_pool || !block_tables || !seq_lens || !query_start)
-    return fail(PA_ERR_INVALID_ARG, "pa_prefill: NULL pointer");
-  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_pool))
-    return fail(PA_ERR_INVALID_ARG, "pa_prefill: out, q and kv_pool must be 16-byte aligned");
+  s = check_prefill_args("pa_prefill", out, q, kv_pool, block_tables, max_blocks_per_seq, seq_lens, query_start,
+                         num_seqs, num_tokens, num_heads, scale, pool, max_query_len);
+  if (s != PA_OK || num_seqs == 0 || max_query_len == 0) return s;
   pagedkv::PrefillParams p;
   p.out = out;
   p.q = q;
@@ -375,6 +386,7 @@ pa_status pa_prefill(void* out, const void* q, const void* kv_pool, const int32_
   p.max_blocks = max_blocks_per_seq;
   p.num_heads = num_heads;
   p.num_kv_heads = pool.num_kv_heads;
+  const int32_t G = num_heads / pool.num_kv_heads;
   p.group = G;
   p.num_blocks = pool.num_blocks;
   p.tile_tokens = 64 / G;
@@ -387,7 +399,7 @@ pa_status pa_prefill(void* out, const void* q, const void* kv_pool, const int32_
   return pagedkv::launch_prefill_bf16_d128(kv_pool, pool.num_blocks, p, num_seqs, (cudaStream_t)stream);
 #else
   p.tile_tokens = 128 / G;
-  return pagedkv::launch_prefill_tc(kv_pool, pool.num_blocks, p, num_seqs, (cudaStream_t)stream);
+  return pagedkv::launch_prefill_tc<>(kv_pool, pool.num_blocks, p, num_seqs, (cudaStream_t)stream);
 #endif
 }
 
@@ -588,6 +600,41 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int3
                                 : pagedkv::launch_decode_q8_code<__nv_bfloat16, 64>(p, pool.dtype, st);
   return pool.head_dim == 128 ? pagedkv::launch_decode_q8_code<float, 128>(p, pool.dtype, st)
                               : pagedkv::launch_decode_q8_code<float, 64>(p, pool.dtype, st);
+}
+
+pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start,
+                        int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale, pa_pool_desc pool,
+                        int32_t max_query_len, void* stream) {
+  const char* fn = "pa_prefill_q8";
+  pa_status s = check_pool(pool, fn, PoolTypes::kQ8);
+  if (s != PA_OK) return s;
+  if (pool.head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d (only 128)", fn, pool.head_dim);
+  s = check_prefill_args(fn, out, q, kv_pool, block_tables, max_blocks_per_seq, seq_lens, query_start, num_seqs,
+                         num_tokens, num_heads, scale, pool, max_query_len);
+  if (s != PA_OK) return s;
+  // the kernel takes the maximum of the raw scores before it scales them
+  if (scale < 0.f) return fail(PA_ERR_INVALID_ARG, "%s: scale is negative", fn);
+  if (num_seqs == 0 || max_query_len == 0) return PA_OK;
+  pagedkv::PrefillParams p = {};
+  p.out = out;
+  p.q = q;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.query_start = query_start;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_heads = num_heads;
+  p.num_kv_heads = pool.num_kv_heads;
+  p.group = num_heads / pool.num_kv_heads;
+  p.num_blocks = pool.num_blocks;
+  p.tile_tokens = 128 / p.group;
+  p.max_query_len = max_query_len;
+  p.num_tokens = num_tokens;
+  p.scale_log2 = scale * pagedkv::kLog2e;
+  p.q8 = pagedkv::q8_layout(pool.num_kv_heads, pool.head_dim);
+  cudaStream_t st = (cudaStream_t)stream;
+  return pool.dtype == PA_Q8_INT8 ? pagedkv::launch_prefill_tc<pagedkv::CodeInt8>(kv_pool, pool.num_blocks, p, num_seqs, st)
+                                  : pagedkv::launch_prefill_tc<pagedkv::CodeE4m3>(kv_pool, pool.num_blocks, p, num_seqs, st);
 }
 
 }  // extern "C"

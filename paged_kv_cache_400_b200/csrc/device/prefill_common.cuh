@@ -3,7 +3,7 @@
 // query_start[b+1] - query_start[b] tokens are the queries.
 #pragma once
 
-#include "common.cuh"
+#include "q8_common.cuh"
 
 namespace pagedkv {
 
@@ -22,6 +22,7 @@ struct PrefillParams {
   int32_t max_query_len;
   int32_t num_tokens;           // rows of q / out
   float scale_log2;
+  Q8Layout q8;                  // 8-bit pools
 };
 
 }  // namespace pagedkv

@@ -56,10 +56,25 @@
 // memory before it exits. Phase tracking: every mbarrier is waited on at most
 // one completion ahead of the last one its waiter consumed, so a parity wait
 // is never ambiguous.
+//
+// 8-bit pools (Code != void, see q8_common.cuh): K and V stages are the codes
+// as bf16, which holds every int8 and e4m3 code exactly, so the tensor-core
+// side is the same. The producers are four warps, one block slot of the tile
+// each, that read codes with plain 16-byte loads a tile ahead, convert them in
+// registers and store them where TMA would have put the rows; whatever codes
+// lie behind the sequence's end are finite and masked. The scales stay fp32: a
+// block's K scale k_b multiplies its 16 columns of S in the exponent's argument,
+// its V scale v_b enters there too,
+//     P = 2^(scale k_b s + log2 v_b - m) = v_b p,   l += (sum of the block's P) / v_b,
+// so both cost no instruction per element; m is the running maximum of the
+// whole argument. Zero V scales count as 1 over a zeroed tile.
 #pragma once
+
+#include <type_traits>
 
 #include "decode_staged.cuh"
 #include "prefill_common.cuh"
+#include "q8_common.cuh"
 #include "tcgen05.cuh"
 
 namespace pagedkv {
@@ -73,10 +88,10 @@ constexpr float kTcRescaleLog2 = 8.0f;            // raise the reference max pas
 
 // Two query tiles of 128 rows share every staged KV tile: one CTA per SM (all
 // 512 tensor-memory columns, 225 KB of shared memory), a 4-deep KV ring.
-template <int kQTiles>
+template <int kQTiles, bool kQ8 = false>
 struct TcConfig {
   static constexpr int kStages = 4;
-  static constexpr int kProducers = 2;              // producer warps, each stages half of every KV tile
+  static constexpr int kProducers = kQ8 ? 4 : 2;    // producer warps, each stages its part of every KV tile
   static constexpr int kSoftmaxWarps = kQTiles * 4;
   static constexpr int kProducerWarp = kQTiles * 4;          // first producer warp
   static constexpr int kMmaWarp = kQTiles * 4 + kProducers;  // first of kQTiles issuer warps, one per tile
@@ -95,8 +110,9 @@ struct TcUnit {
   int32_t b, g, unit, q0, n, L;
 };
 
-template <int kQTiles, int kStages>
+template <int kQTiles, int kStages, bool kQ8>
 struct PrefillTcShared {
+  float4 block_scale[kQ8 ? kStages : 1][kTcBlocksPerTile];  // scale k_b log2 e, log2 v_b, 1 / v_b of each staged block
   alignas(16) uint4 clc_resp;    // response of the last cancellation request
   int32_t unit_desc[2][6];       // published units (TcUnit), two slots
   uint64_t clc_bar;              // cancellation response written
@@ -114,6 +130,28 @@ struct PrefillTcShared {
   uint64_t staged[kQTiles];      // tile t's half rows written to staging (one arrival per softmax warp)
   uint32_t tmem_base;
 };
+
+// Four codes of one word -> two bf16 pairs, codes 0, 1 and 2, 3; exact, and
+// finite for every bit pattern.
+// int8: 128 + (c & 127), less 128 or, for a negative code, 256.
+__device__ __forceinline__ void q8_to_bf16(CodeInt8, uint32_t w, uint32_t& p, uint32_t& q) {
+  const uint32_t m = w & 0x7f7f7f7fu, sign = w & 0x80808080u;
+  asm("sub.rn.bf16x2 %0, %1, %2;"
+      : "=r"(p)
+      : "r"(__byte_perm(m, 0x43434343u, 0x4140)), "r"(__byte_perm(sign, 0x43434343u, 0x4140)));
+  asm("sub.rn.bf16x2 %0, %1, %2;"
+      : "=r"(q)
+      : "r"(__byte_perm(m, 0x43434343u, 0x4342)), "r"(__byte_perm(sign, 0x43434343u, 0x4342)));
+}
+// e4m3: exponent and significand in the low bits of bf16's fields stand for
+// value * 2^-120, its subnormals included.
+__device__ __forceinline__ void q8_to_bf16(CodeE4m3, uint32_t w, uint32_t& p, uint32_t& q) {
+  const uint32_t m = w & 0x7f7f7f7fu, sign = w & 0x80808080u;
+  const uint32_t a = (__byte_perm(m, 0, 0x4140) << 4) + __byte_perm(sign, 0, 0x1404);
+  const uint32_t b = (__byte_perm(m, 0, 0x4342) << 4) + __byte_perm(sign, 0, 0x3424);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(a), "r"(0x7b807b80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(b), "r"(0x7b807b80u));
+}
 
 // 2^x on the special-function unit (approximate, flushes results below 2^-126
 // to zero).
@@ -302,15 +340,16 @@ __device__ __forceinline__ int32_t unit_tiles(const TcUnit& u, int32_t QT, int32
   return (nblocks + kTcBlocksPerTile - 1) / kTcBlocksPerTile;
 }
 
-template <int kQTiles>
-__global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
+template <int kQTiles, typename Code = void>
+__global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap out_map, PrefillParams p, const uint4* __restrict__ pool,
                       int32_t num_seqs) {
-  using Cfg = TcConfig<kQTiles>;
+  constexpr bool kQ8 = !std::is_void<Code>::value;
+  using Cfg = TcConfig<kQTiles, kQ8>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ PrefillTcShared<kQTiles, S> sh;
+  __shared__ PrefillTcShared<kQTiles, S, kQ8> sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = smem;
   uint8_t* kv_smem = smem + kQTiles * kTcQBytes;
@@ -351,7 +390,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
       mbar_init(&sh.staged[t], 4);
     }
     fence_barrier_init();
-    prefetch_tensormap(&pool_map);
+    if constexpr (!kQ8) prefetch_tensormap(&pool_map);
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&out_map);
   }
@@ -378,7 +417,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
   };
 
   if (warp >= Cfg::kProducerWarp && warp < Cfg::kMmaWarp) {
-    // ---- producers: warp pw stages blocks 2 pw, 2 pw + 1 of every 64-key tile -------
+    // ---- producers: warp pw stages blocks 2 pw, 2 pw + 1 of every 64-key tile (8-bit: block pw)
     const int32_t pw = warp - Cfg::kProducerWarp;
 
     // stages the unit's KV tiles (global tile index jkv0 + j) into the ring
@@ -387,6 +426,88 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
       int32_t nblocks;
       const int32_t nt_max = unit_tiles<kQTiles>(u, QT, nt, nblocks);
       const int32_t* table = p.block_tables + (size_t)u.b * p.max_blocks;
+      if constexpr (kQ8) {
+        // ids of this warp's slot in batches of 32 tiles, the next batch in flight
+        auto load_ids = [&](int32_t k) -> int32_t {
+          const int32_t bi = (k * 32 + lane) * kTcBlocksPerTile + pw;
+          return bi < nblocks ? __ldg(table + bi) : -1;
+        };
+        // A lane's 16 codes of every 512 bytes (4 rows): the 8 lanes of a store
+        // phase hold two neighbouring rows' even chunks, which the swizzle
+        // spreads over all banks.
+        const int32_t row = ((lane >> 2) & 1) + 2 * (lane >> 4);
+        const int32_t c16 = (lane & 3) + 4 * ((lane >> 3) & 1);
+        uint4 code[8];  // K rows, V rows of the block
+        float ks, vs;
+        int32_t ids = load_ids(0), ids_next = load_ids(1);
+        auto load_codes = [&](int32_t j) {
+          if (j > 0 && (j & 31) == 0) {
+            ids = ids_next;
+            ids_next = load_ids(j / 32 + 1);
+          }
+          const int32_t blk = __shfl_sync(0xffffffffu, ids, j & 31);
+          const bool in = j * kTcBlocksPerTile + pw < nblocks;
+          if (in && blk >= 0 && blk < p.num_blocks) {
+            const uint8_t* base = reinterpret_cast<const uint8_t*>(pool) + (size_t)blk * p.q8.block_bytes;
+            const uint8_t* at = base + (size_t)u.g * 2048 + row * 128 + c16 * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              code[i] = __ldg(reinterpret_cast<const uint4*>(at + 512 * i));
+              code[4 + i] = __ldg(reinterpret_cast<const uint4*>(at + (size_t)p.num_kv_heads * 2048 + 512 * i));
+            }
+            const float* sc = reinterpret_cast<const float*>(base + p.q8.scale_offset) + u.g;
+            ks = __ldg(sc);
+            vs = __ldg(sc + p.num_kv_heads);
+          } else {
+            if (in && lane == 0) raise_device_error(PA_DEVERR_BLOCK);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) code[i] = make_uint4(0, 0, 0, 0);
+            ks = vs = 1.f;
+          }
+        };
+        load_codes(0);
+        for (int32_t j = 0; j < nt_max; ++j) {
+          const uint32_t J = jkv0 + (uint32_t)j;
+          const uint32_t s = J % S;
+          uint4 c[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = code[i];
+          const float k_b = ks, v_b = vs;
+          if (j + 1 < nt_max) load_codes(j + 1);
+          if (J >= (uint32_t)S) {
+            const bool ok = mbar_wait_bounded(&sh.kv_empty[s], (J / S - 1) & 1u, kWaitLimitNs);
+            if (__any_sync(0xffffffffu, !ok)) {
+              if (lane == 0) raise_device_error(PA_DEVERR_TIMEOUT);
+              return false;
+            }
+          }
+          if (v_b == 0.f) {
+#pragma unroll
+            for (int i = 4; i < 8; ++i) c[i] = make_uint4(0, 0, 0, 0);
+          }
+          uint8_t* st = kv_smem + s * kTcStageBytes;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int32_t key = pw * 16 + 4 * (i & 3) + row;
+            uint8_t* line = st + tc_region(i >> 2, c16 >> 2) + key * 128;
+            const int32_t ch = 2 * (c16 & 3);
+            uint4 lo, hi;
+            q8_to_bf16(Code{}, c[i].x, lo.x, lo.y);
+            q8_to_bf16(Code{}, c[i].y, lo.z, lo.w);
+            q8_to_bf16(Code{}, c[i].z, hi.x, hi.y);
+            q8_to_bf16(Code{}, c[i].w, hi.z, hi.w);
+            *reinterpret_cast<uint4*>(line + ((ch ^ (key & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (key & 7)) << 4)) = hi;
+          }
+          if (lane == 0)
+            sh.block_scale[s][pw] = make_float4(p.scale_log2 * k_b, v_b > 0.f ? log2f(v_b) : 0.f,
+                                                v_b > 0.f ? 1.f / v_b : 1.f, 0.f);
+          fence_proxy_async_smem();  // the stage's writes before the MMAs read them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kv_full[s]);
+        }
+        return true;
+      }
       // block ids in batches of 32 (8 KV tiles), lane l holding entry l of its
       // batch; the next batch is in flight while the current one is staged
       constexpr int32_t kTilesPerBatch = 32 / kTcBlocksPerTile;
@@ -690,8 +811,9 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
     const uint32_t lane_base = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16);
     uint8_t* stage = out_smem + t * (kTcQBytes / 2);  // half of this tile's output rows, in the Q tile layout
     const bool leader = r == 0;                 // issues the tile's output stores
-    uint32_t k = 0;   // units taken
-    uint32_t js = 0;  // this tile's KV steps of the earlier units
+    uint32_t k = 0;    // units taken
+    uint32_t jkv = 0;  // KV tiles of the earlier units
+    uint32_t js = 0;   // this tile's KV steps of the earlier units
     uint32_t ne = 0;  // this tile's staged output halves so far
     bool ok = true;
     for (;;) {
@@ -704,7 +826,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sh.unit_empty[k & 1]);
       if (u.n < 0) break;
       int32_t nt[kQTiles], nblocks;
-      unit_tiles<kQTiles>(u, QT, nt, nblocks);
+      const int32_t nt_max = unit_tiles<kQTiles>(u, QT, nt, nblocks);
       const int32_t ntt = (kQTiles == 1 || t == 0) ? nt[0] : nt[kQTiles - 1];
       const int32_t ctx = u.L - u.n;
       const int32_t tb = u.unit * U + t * QT;
@@ -733,11 +855,31 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
         }
         // tile max of the raw scores: three-input max, four independent chains
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mt;
+        // 8-bit: the blocks' scales, written before the arrivals on kv_full that
+        // the MMAs of S have waited for (this stage is refilled after P_j)
+        const float4* bsc = sh.block_scale[kQ8 ? (jkv + (uint32_t)j) % S : 0];
+        if constexpr (kQ8) {
+          const uint32_t J = jkv + (uint32_t)j;
+          const bool staged = mbar_wait_bounded(&sh.kv_full[J % S], (J / S) & 1u, kWaitLimitNs);
+          if (__any_sync(0xffffffffu, !staged)) {
+            ok = false;
+            break;
+          }
+          // a chain per block; a masked column times a zero scale is NaN, which fmaxf drops
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          m4[c & 3] = max3(m4[c & 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
-        float mt = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-        mt *= p.scale_log2;
+          for (int c = 0; c < 32; ++c)
+            m4[c >> 3] = max3(m4[c >> 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+          mt = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kTcBlocksPerTile; ++b) mt = fmaxf(mt, fmaf(m4[b], bsc[b].x, bsc[b].y));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            m4[c & 3] = max3(m4[c & 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+          mt = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          mt *= p.scale_log2;
+        }
         if (j == 0) {
           m_ref = mt;  // key 0 is never masked: finite
         } else {
@@ -766,12 +908,25 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
         }
         // p = 2^(s * scale - m) on the special-function unit; the exponent
         // arguments and the row sum two columns per instruction
-        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-        const float2 neg_m2 = make_float2(-m_ref, -m_ref);
+        float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        float2 neg_m2 = make_float2(-m_ref, -m_ref);
         uint32_t pw[32];
         float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float rv = 0.f;  // 8-bit: 1 / V scale of the block before column 2 c
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
+          if constexpr (kQ8) {
+            if (c % 8 == 0) {
+              if (c > 0) {
+                l = fmaf((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y), rv, l);
+                sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+              }
+              const float4 b = bsc[c / 8];
+              scale2 = make_float2(b.x, b.x);
+              neg_m2 = make_float2(b.y - m_ref, b.y - m_ref);
+              rv = b.z;
+            }
+          }
           const float2 x =
               fma2(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, neg_m2);
           float p0 = ex2_sfu(x.x);
@@ -783,7 +938,8 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
           sum2[c & 1] = add2(sum2[c & 1], make_float2(p0, p1));
           pw[c] = pack_bf16x2(p0, p1);
         }
-        l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
+        if constexpr (kQ8) l = fmaf((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y), rv, l);
+        else l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
         tmem_st32(sbuf, pw);
         tmem_wait_st();
         tc_fence_before_sync();
@@ -854,6 +1010,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles>::kThreads, 1)
           }
         }
       }
+      jkv += (uint32_t)nt_max;
       js += (uint32_t)ntt;
       ++k;
       if (!ok) break;
@@ -889,19 +1046,23 @@ inline pa_status encode_q_map(const void* q, int32_t num_heads, int32_t num_toke
   return PA_OK;
 }
 
+template <typename Code = void>
 inline pa_status launch_prefill_tc(const void* pool, int32_t num_blocks, const PrefillParams& p, int32_t num_seqs,
                                    cudaStream_t st) {
-  using Cfg = TcConfig<kTcQTiles>;
+  constexpr bool kQ8 = !std::is_void<Code>::value;
+  using Cfg = TcConfig<kTcQTiles, kQ8>;
+  const char* fn = kQ8 ? "pa_prefill_q8" : "pa_prefill";
   CUtensorMap pool_map, q_map, out_map;
-  pa_status s = encode_pool_map(pool, p.num_kv_heads, num_blocks, &pool_map, 1);
-  if (s != PA_OK) return s;
-  s = encode_q_map(p.q, p.num_heads, p.num_tokens, p.group, &q_map);
+  pa_status s = encode_q_map(p.q, p.num_heads, p.num_tokens, p.group, &q_map);
   if (s != PA_OK) return s;
   s = encode_q_map(p.out, p.num_heads, p.num_tokens, p.group, &out_map);
   if (s != PA_OK) return s;
+  if constexpr (kQ8) pool_map = q_map;  // not used: codes are read by plain loads
+  else s = encode_pool_map(pool, p.num_kv_heads, num_blocks, &pool_map, 1);
+  if (s != PA_OK) return s;
   static PerDevice<int32_t> smem_set;
-  cudaError_t attr = set_smem_once(smem_set, prefill_tc_kernel<kTcQTiles>, Cfg::kSmem);
-  if (attr != cudaSuccess) return fail(PA_ERR_CUDA, "pa_prefill: %s", cudaGetErrorString(attr));
+  cudaError_t attr = set_smem_once(smem_set, prefill_tc_kernel<kTcQTiles, Code>, Cfg::kSmem);
+  if (attr != cudaSuccess) return fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(attr));
   // one CTA per unit (an upper bound on the units of well-formed query
   // ranges: every sequence has at most max_query_len new tokens, and together
   // at most num_tokens); running CTAs cancel most of them and take their units
@@ -910,11 +1071,11 @@ inline pa_status launch_prefill_tc(const void* pool, int32_t num_blocks, const P
                                           ((int64_t)p.num_tokens + (int64_t)num_seqs * (U - 1)) / U);
   const int64_t ctas = units * p.num_kv_heads;
   if (ctas <= 0) return PA_OK;
-  if (ctas > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "pa_prefill: %lld work units", (long long)ctas);
-  prefill_tc_kernel<kTcQTiles><<<(unsigned)ctas, Cfg::kThreads, Cfg::kSmem, st>>>(
+  if (ctas > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "%s: %lld work units", fn, (long long)ctas);
+  prefill_tc_kernel<kTcQTiles, Code><<<(unsigned)ctas, Cfg::kThreads, Cfg::kSmem, st>>>(
       pool_map, q_map, out_map, p, reinterpret_cast<const uint4*>(pool), num_seqs);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_prefill: launch failed: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return PA_OK;
 }
 

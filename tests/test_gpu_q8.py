@@ -362,3 +362,139 @@ def test_decode_refusals():
     with pytest.raises(pk.PagedKVError) as e:
         pk.pa_decode_q8(o, q, p, wide, ln, 0.1, 9600)
     assert e.value.status == "WORKSPACE"
+
+
+# ---- prefill ---------------------------------------------------------------------
+def prefill(p, q, tables, lens, start, scale, max_new, out=None):
+    q = q.to(DEV)
+    out = torch.full_like(q, float("nan")) if out is None else out
+    pk.pa_prefill_q8(out, q, p, torch.from_numpy(tables).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                     torch.tensor(start, dtype=torch.int32, device=DEV), scale, max_new)
+    return out
+
+
+def check_prefill(heads_kv, group, code, lens, news, spread=0.5, seed=0, scale=128 ** -0.5):
+    blocks = sum((n + 15) // 16 for n in lens) + 3
+    p = make_pool(blocks, heads_kv, 128, code, seed, spread)
+    tables = tables_for(lens, blocks, None, seed)
+    codes, scales = poison(p, tables, lens)
+    start = np.concatenate([[0], np.cumsum(news)]).tolist()
+    q = rows(start[-1] + 5, heads_kv * group, 128, "bf16", seed + 1, 0.3)  # five rows behind the last sequence
+    out = prefill(p, q, tables, lens, start, scale, max(news))
+    assert pk.pa_get_device_error() == 0
+    assert torch.isnan(out[start[-1]:]).all()
+    # a probability times its V scale as bf16 (8 bits, fp32's exponents), sums over the whole sequence
+    check_rows(out, q, lens, news, start, codes, scales, tables, p, "bf16", scale, 2.0 ** -8, max(lens), 2.0 ** -100)
+
+
+@CODE
+@pytest.mark.parametrize("heads_kv,group", [(1, 1), (3, 2), (2, 4), (1, 8), (2, 16)])
+def test_prefill_prompts(heads_kv, group, code):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 100, 129, 200, 257]
+    check_prefill(heads_kv, group, code, lens, lens, seed=group)
+
+
+@CODE
+@pytest.mark.parametrize("heads_kv,group", [(2, 1), (2, 4), (1, 16)])
+def test_prefill_chunks(heads_kv, group, code):
+    """New tokens behind cached contexts, single tokens and empty requests among them."""
+    check_prefill(heads_kv, group, code, [700, 16, 33, 65, 1, 0, 500, 64, 128, 1025], [300, 1, 17, 64, 1, 0, 1, 0, 33, 70],
+                  seed=2)
+
+
+@CODE
+def test_prefill_scales_far_apart(code):
+    check_prefill(2, 4, code, [1, 16, 40, 200, 900], [1, 16, 20, 100, 60], spread=5.0, seed=3)
+
+
+@CODE
+def test_prefill_many_sequences(code):
+    """More sequences than the launch sorts by length, more units than SMs."""
+    r = np.random.RandomState(5)
+    lens = r.randint(1, 150, 200)
+    check_prefill(2, 8, code, lens.tolist(), (1 + (lens - 1) * r.rand(200)).astype(int).tolist(), seed=4)
+
+
+@CODE
+def test_prefill_zero_scales(code):
+    p = make_pool(20, 2, 128, code, 1)
+    lens = [130, 33]
+    tables = tables_for(lens, 20, 9)
+    p.scales[torch.from_numpy(tables[0, [0, 1, 4]]).long().to(DEV)] = 0   # zero K and V tiles
+    p.scales[torch.from_numpy(tables[1, :3]).long().to(DEV), 1] = 0       # every V tile zero
+    codes, scales = host(p)
+    q = rows(163, 8, 128, "bf16", 3)
+    for scale in (0.1, 0.0):
+        out = prefill(p, q, tables, lens, [0, 130, 163], scale, 130)
+        assert pk.pa_get_device_error() == 0
+        check_rows(out, q, lens, lens, [0, 130], codes, scales, tables, p, "bf16", scale, 2.0 ** -8, 130, 2.0 ** -100)
+        assert not out[130:].any()
+
+
+@CODE
+def test_prefill_bad_blocks_and_lengths(code):
+    p = make_pool(60, 2, 128, code, 1)
+    lens, news = [100, 90, 33, 300, 64], [50, 90, 40, 10, 64]             # 2: more new tokens than tokens; 3: too long
+    tables = tables_for([100, 90, 33, 16, 64], 60, 8)
+    start = np.concatenate([[0], np.cumsum(news)]).tolist()
+    q = rows(start[-1], 4, 128, "bf16", 3)
+    out = prefill(p, q, tables, lens, start, 0.1, 90)
+    assert pk.pa_get_device_error() == pk.PA_DEVERR_SEQLEN
+    codes, scales = host(p)
+    assert torch.isnan(out[start[2]:start[4]]).all()
+    for b in (0, 1, 4):
+        check_rows(out[start[b]:start[b + 1]], q[start[b]:start[b + 1]], [lens[b]], [news[b]], [0], codes, scales,
+                   tables[b:b + 1], p, "bf16", 0.1, 2.0 ** -8, 100, 2.0 ** -100)
+    tables[0, 2], tables[1, 0] = 60, -1
+    out2 = prefill(p, q, tables, [100, 90, 40, 10, 64], start, 0.1, 90)
+    assert pk.pa_get_device_error() == pk.PA_DEVERR_BLOCK
+    assert torch.equal(out2[start[4]:], out[start[4]:]) and torch.isfinite(out2[:start[2]]).all()
+
+
+def test_prefill_agrees_with_decode_and_runs_in_a_graph():
+    """A single new token is a decode step; a captured call replays with new lengths and tables."""
+    lens = [400, 77, 16, 1, 250]
+    p = make_pool(60, 4, 128, "int8", 8)
+    tables = tables_for(lens, 60, 26)
+    q = rows(5, 16, 128, "bf16", 9)
+    a = prefill(p, q, tables, lens, range(6), 0.09, 1)
+    b = decode(p, q, tables, lens, 416, 0.09)
+    codes, scales = host(p)
+    for x in (a, b):
+        check_rows(x, q, lens, [1] * 5, range(5), codes, scales, tables, p, "bf16", 0.09, 2.0 ** -8, 400)
+    dq, dt = q.to(DEV), torch.from_numpy(tables).to(DEV)
+    dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ds = torch.arange(6, dtype=torch.int32, device=DEV)
+    out = torch.empty_like(dq)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pk.pa_prefill_q8(out, dq, p, dt, dl, ds, 0.09, 4)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, a)
+    dl.copy_(torch.tensor([300, 77, 16, 4, 200], dtype=torch.int32))
+    ds.copy_(torch.tensor([0, 1, 1, 1, 5, 5], dtype=torch.int32))
+    out.fill_(0)
+    g.replay()
+    want = prefill(p, q, dt.cpu().numpy(), dl.tolist(), ds.tolist(), 0.09, 4, torch.zeros_like(dq))
+    assert torch.equal(out, want) and pk.pa_get_device_error() == 0
+
+
+def test_prefill_refusals():
+    p = make_pool(8, 2, 128, "int8", 1)
+    q = rows(3, 4, 128, "bf16", 1).to(DEV)
+    t = torch.zeros(1, 4, dtype=torch.int32, device=DEV)
+    ln, st = torch.full((1,), 3, dtype=torch.int32, device=DEV), torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    o = torch.empty_like(q)
+    for a in [(o, q.float()), (o.float(), q), (o[:2], q), (o, q.cpu())]:
+        with pytest.raises(ValueError):
+            pk.pa_prefill_q8(a[0], a[1], p, t, ln, st, 0.1, 3)
+    with pytest.raises(ValueError):
+        pk.pa_prefill_q8(o, q, p, t, ln, st[:1], 0.1, 3)
+    small = make_pool(8, 2, 64, "int8", 1)
+    with pytest.raises(pk.PagedKVError) as e:
+        pk.pa_prefill_q8(o[..., :64].contiguous(), q[..., :64].contiguous(), small, t, ln, st, 0.1, 3)
+    assert e.value.status == "UNSUPPORTED"
+    with pytest.raises(pk.PagedKVError) as e:
+        pk.pa_prefill_q8(o, q, p, t, ln, st, -0.1, 3)
+    assert e.value.status == "INVALID_ARG"

@@ -122,3 +122,15 @@ def test_decode_refuses_on_host():
     assert call(mb=256, ml=4096) == 9 and call(mb=256, ml=4096, ws=C.c_void_p(256), wb=need - 1) == 9
     assert call(mb=256, ml=4096, ws=C.c_void_p(128), wb=need) == 1
     assert call(ns=0, out=None) == 0
+
+
+def test_prefill_refuses_on_host():
+    L = bd.lib()
+    call = lambda out=VP, q=VP, pool=VP, mb=4, ns=2, nt=64, H=8, scale=0.1, d=desc(heads=2), mq=40: \
+        L.pa_prefill_q8(out, q, pool, VP, mb, VP, VP, ns, nt, H, scale, d, mq, None)
+    assert call(d=desc(dim=64)) == 2 and call(d=desc(dtype=bd.PA_BF16)) == 2
+    assert call(H=6) == 2 and call(H=7) == 1 and call(H=64) == 2
+    assert call(scale=-0.1) == 1 and call(scale=float("nan")) == 1
+    assert call(mq=65) == 1 and call(mq=-1) == 1 and call(mb=2) == 1 and call(ns=-1) == 1 and call(ns=70000) == 2
+    assert call(out=None) == 1 and call(q=C.c_void_p(8)) == 1
+    assert call(ns=0, out=None) == 0 and call(mq=0, out=None) == 0
