@@ -425,18 +425,39 @@ class Q8Pool:
         return self.buf[:, raw:raw + 8 * self.num_kv_heads].view(torch.float32).unflatten(1, (2, self.num_kv_heads))
 
 
-def _here(t: torch.Tensor, name: str, *dtypes) -> C.c_void_p:
-    """As _dev, for a tensor that must lie on the current device (the library
-    launches there) and have one of `dtypes`."""
-    p = _dev(t, name)
-    if dtypes and t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return p
+def _here(t: torch.Tensor, name: str, dev: int, dtype) -> int:
+    """Address of a contiguous tensor of `dtype` on the current device `dev`
+    (the library launches there). A call makes several of these checks and can
+    be shorter than they are, so the good case is kept to three queries."""
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        _dev(t, name, dtype)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _current_device(t: torch.Tensor, name: str) -> int:
+    """The current device, on which t must lie."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _launch_stream(stream, dev: int):
+    """As _stream; the current stream's handle is asked for directly, without
+    the Stream object around it (3.4 us of a call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 _IO = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
+
+
+def _io(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _IO:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return _IO[t.dtype]
 
 
 def _q8_pool(pool) -> Q8Pool:
@@ -455,9 +476,10 @@ def pa_reshape_and_cache_q8(k, v, pool, slot_mapping, stream=None):
         raise ValueError("k, v must be [num_tokens][num_kv_heads][head_dim]")
     if n == 0:
         return
+    io, dev = _io(k, "k"), _current_device(k, "k")
     _check("pa_reshape_and_cache_q8", lib().pa_reshape_and_cache_q8(
-        _here(k, "k", *_IO), _here(v, "v", k.dtype), _here(pool.buf, "pool"),
-        _here(slot_mapping, "slot_mapping", torch.int64), n, pool.desc, _IO[k.dtype], _stream(stream)))
+        _here(k, "k", dev, k.dtype), _here(v, "v", dev, k.dtype), _here(pool.buf, "pool", dev, torch.uint8),
+        _here(slot_mapping, "slot_mapping", dev, torch.int64), n, pool.desc, io, _launch_stream(stream, dev)))
 
 
 def pa_decode_q8(out, q, pool, block_tables, seq_lens, scale, max_seq_len, workspace=None, stream=None):
@@ -469,14 +491,14 @@ def pa_decode_q8(out, q, pool, block_tables, seq_lens, scale, max_seq_len, works
         raise ValueError("q, out must be [num_seqs][num_heads][head_dim]")
     if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_tables must be [num_seqs][max_blocks], seq_lens [num_seqs]")
-    ws_ptr, ws_bytes = C.c_void_p(0), 0
+    io, dev, i = _io(q, "q"), _current_device(q, "q"), torch.int32
+    ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        ws_ptr, ws_bytes = _here(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = _here(workspace, "workspace", dev, workspace.dtype), workspace.nbytes
     _check("pa_decode_q8", lib().pa_decode_q8(
-        _here(out, "out", q.dtype), _here(q, "q", *_IO), _here(pool.buf, "pool"),
-        _here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-        _here(seq_lens, "seq_lens", torch.int32), B, H, float(scale), pool.desc, _IO[q.dtype], ws_ptr, ws_bytes,
-        int(max_seq_len), _stream(stream)))
+        _here(out, "out", dev, q.dtype), _here(q, "q", dev, q.dtype), _here(pool.buf, "pool", dev, torch.uint8),
+        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i), B, H,
+        float(scale), pool.desc, io, ws_ptr, ws_bytes, int(max_seq_len), _launch_stream(stream, dev)))
 
 
 def pa_prefill_q8(out, q, pool, block_tables, seq_lens, query_start, scale, max_query_len, stream=None):
@@ -490,11 +512,12 @@ def pa_prefill_q8(out, q, pool, block_tables, seq_lens, query_start, scale, max_
     if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.shape != (B,) \
             or query_start.shape != (B + 1,):
         raise ValueError("block_tables [num_seqs][max_blocks], seq_lens [num_seqs], query_start [num_seqs+1]")
+    dev, i, bf16 = _current_device(q, "q"), torch.int32, torch.bfloat16
     _check("pa_prefill_q8", lib().pa_prefill_q8(
-        _here(out, "out", torch.bfloat16), _here(q, "q", torch.bfloat16), _here(pool.buf, "pool"),
-        _here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-        _here(seq_lens, "seq_lens", torch.int32), _here(query_start, "query_start", torch.int32), B, T, H,
-        float(scale), pool.desc, int(max_query_len), _stream(stream)))
+        _here(out, "out", dev, bf16), _here(q, "q", dev, bf16), _here(pool.buf, "pool", dev, torch.uint8),
+        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i),
+        _here(query_start, "query_start", dev, i), B, T, H, float(scale), pool.desc, int(max_query_len),
+        _launch_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------------------
@@ -537,14 +560,14 @@ def pa_tables_extend(block_tables, seq_lens, new_tokens, free_ring, ring_state, 
         raise ValueError("query_start [num_seqs + 1], slot_mapping [num_slots], free_ring [ring_size]")
     if workspace is None:
         workspace = alloc_tables_workspace(B, seq_lens.device)
-    i = torch.int32
+    dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
     _check("pa_tables_extend", lib().pa_tables_extend(
-        _here(block_tables, "block_tables", i), block_tables.shape[1], _here(seq_lens, "seq_lens", i),
-        _here(new_tokens, "new_tokens", i), B, _here(free_ring, "free_ring", i), free_ring.numel(),
-        _here(ring_state, "ring_state", i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", i),
-        _here(query_start, "query_start", i), _here(slot_mapping, "slot_mapping", torch.int64),
-        slot_mapping.numel(), int(row_tokens), _here(ring_state_out, "ring_state_out", i),
-        _here(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i),
+        _here(new_tokens, "new_tokens", dev, i), B, _here(free_ring, "free_ring", dev, i), free_ring.shape[0],
+        _here(ring_state, "ring_state", dev, i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", dev, i),
+        _here(query_start, "query_start", dev, i), _here(slot_mapping, "slot_mapping", dev, torch.int64),
+        slot_mapping.shape[0], int(row_tokens), _here(ring_state_out, "ring_state_out", dev, i),
+        _here(workspace, "workspace", dev, workspace.dtype), workspace.nbytes, _launch_stream(stream, dev)))
 
 
 def pa_tables_release(block_tables, seq_lens, finished, free_ring, ring_state, seq_lens_out, ring_state_out,
@@ -556,13 +579,13 @@ def pa_tables_release(block_tables, seq_lens, finished, free_ring, ring_state, s
         raise ValueError("free_ring [ring_size]")
     if workspace is None:
         workspace = alloc_tables_workspace(B, seq_lens.device)
-    i = torch.int32
+    dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
     _check("pa_tables_release", lib().pa_tables_release(
-        _here(block_tables, "block_tables", i), block_tables.shape[1], _here(seq_lens, "seq_lens", i),
-        _here(finished, "finished", i), B, _here(free_ring, "free_ring", i), free_ring.numel(),
-        _here(ring_state, "ring_state", i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", i),
-        _here(ring_state_out, "ring_state_out", i), _here(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i),
+        _here(finished, "finished", dev, i), B, _here(free_ring, "free_ring", dev, i), free_ring.shape[0],
+        _here(ring_state, "ring_state", dev, i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", dev, i),
+        _here(ring_state_out, "ring_state_out", dev, i), _here(workspace, "workspace", dev, workspace.dtype),
+        workspace.nbytes, _launch_stream(stream, dev)))
 
 
 def pa_selftest_timeout(limit_ns: int, stream=None):

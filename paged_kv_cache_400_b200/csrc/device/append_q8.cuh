@@ -9,13 +9,15 @@
 // One warp owns a tile, so a scale and the rows under it change together and
 // nothing is summed or ordered across warps: the warp of a block's first token
 // in slot_mapping (its leader) gathers the block's other tokens from the 31
-// entries behind it, and the warps of those other tokens leave at once. A row
-// named twice takes the later token.
+// entries behind it; the other tokens lead nothing. A row named twice takes the
+// later token.
 //
 // Bound by its bytes (reads T * Hkv * D elements twice over for K and V, writes
-// half or a quarter as many) for many tokens, by latency for few: a step of one
-// token per request gives every token a warp per (K|V, head), and all of a
-// tile's rows are loaded before the first is used.
+// half or a quarter as many) for many tokens, by latency for few. A warp looks
+// at a run of entries at once, with the entries before and behind them, and
+// then serves their leaders: the scale and all new rows of a tile are in flight
+// together, 16 bytes a lane, and stay in registers between the maximum and the
+// codes.
 #pragma once
 
 #include "q8_common.cuh"
@@ -23,116 +25,173 @@
 namespace pagedkv {
 
 constexpr int kAppendQ8Warps = 4;
-constexpr int kAppendWindow = 32;  // a block's tokens lie within this many entries
+constexpr int kAppendQ8Run = 16;                   // most entries a warp looks at
 constexpr float kQ8Tiny = 7.888609052210118e-31f;  // 2^-100: below it a tile counts as zeros (1 / s stays finite)
 
-// Warp (4 x + w, head y, kv z) serves the leaders among tokens
-// [per_warp * (4 x + w), + per_warp).
+// Largest magnitude of words of elements, on their bit patterns (which order
+// as the magnitudes do): per word, and as the fp32 pattern of the larger half.
+template <typename T> struct Bits;
+template <> struct Bits<float> {
+  __device__ __forceinline__ static uint32_t max_abs(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+  __device__ __forceinline__ static uint32_t widest(uint32_t m) { return m; }
+  __device__ __forceinline__ static float get(const uint32_t* w, int c) { return __uint_as_float(w[c]); }
+};
+template <> struct Bits<__nv_bfloat16> {
+  __device__ __forceinline__ static uint32_t max_abs(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+  __device__ __forceinline__ static uint32_t widest(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  __device__ __forceinline__ static float get(const uint32_t* w, int c) {
+    return __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
+  }
+};
+
+// Warp (4 x + w, head y, kv z) serves the leaders among entries
+// [run * (4 x + w), + run).
 template <typename T, int D, typename Code>
 __global__ void __launch_bounds__(kAppendQ8Warps * 32)
 append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ pool,
                  const int64_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
-                 Q8Layout lay, int32_t per_warp) {
-  constexpr int PER = D / 32;  // elements of a row per lane
-  using In = Vec<T, PER>;
-  using Codes = Vec<uint8_t, PER>;
-  __shared__ __align__(16) uint8_t row_src[kAppendQ8Warps][16];
+                 Q8Layout lay, int32_t run) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int E = 16 / sizeof(T);     // elements per lane and step
+  constexpr int kLanes = D / E;         // lanes of a row
+  constexpr int kRows = 32 / kLanes;    // rows of a step
+  constexpr int kSteps = 16 / kRows;
+  using Codes = Vec<uint8_t, E>;
+  union Words {  // 16 bytes of a row
+    uint4 q;
+    uint32_t w[4];
+    __device__ __forceinline__ float get(int c) const { return Bits<T>::get(w, c); }
+  };
+  __shared__ uint8_t row_src[kAppendQ8Warps][16];
   const int32_t warp = threadIdx.x >> 5;
   const int32_t lane = threadIdx.x & 31;
   const int32_t h = blockIdx.y;
   const int32_t kv = blockIdx.z;
+  const bool reports = h == 0 && kv == 0;
   const T* src = kv ? v : k;
-  // block of entry t, -1 for padding, an entry outside the list or a bad slot
-  auto block_of = [&](int64_t t, int64_t& s) -> int64_t {
-    s = t >= 0 && t < num_tokens ? __ldg(slots + t) : -1;
-    return s >= 0 && s < num_slots ? s >> 4 : -1;
-  };
-  const int64_t t_first = ((int64_t)blockIdx.x * kAppendQ8Warps + warp) * per_warp;
-  const int64_t t_end = min(t_first + per_warp, (int64_t)num_tokens);
-  for (int64_t t = t_first; t < t_end; ++t) {
-    int64_t s, s_prev, s_next;
-    const int64_t blk_here = block_of(t + lane, s);              // entries t .. t + 31
-    const int64_t blk_prev = block_of(t - 31 + lane, s_prev);    // entries t - 31 .. t (lane 31: t itself)
-    const int64_t blk_next = block_of(t + 32 + lane, s_next);    // entries t + 32 .. t + 63
-    const int64_t blk = __shfl_sync(0xffffffffu, blk_here, 0);
-    if (blk < 0) {
-      if (lane == 0 && s >= num_slots && h == 0 && kv == 0) raise_device_error(PA_DEVERR_SLOT);
-      continue;
-    }
-    if (__any_sync(0xffffffffu, lane < 31 && blk_prev == blk)) continue;  // an earlier entry leads
-    // tokens of the block behind the window are not written
-    if (__any_sync(0xffffffffu, lane < 31 && blk_next == blk) && lane == 0 && h == 0 && kv == 0)
+  const int32_t t0 = (blockIdx.x * kAppendQ8Warps + warp) * run;
+  if (t0 >= num_tokens) return;
+  // entry t's slot, -1 for padding, a bad slot or an entry outside the list
+  auto slot_of = [&](int64_t t) -> int64_t { return t >= 0 && t < num_tokens ? __ldg(slots + t) : -1; };
+  const int64_t raw0 = slot_of((int64_t)t0 + lane), raw_prev = slot_of((int64_t)t0 - 32 + lane);
+  const int64_t raw1 = slot_of((int64_t)t0 + 32 + lane), raw2 = slot_of((int64_t)t0 + 64 + lane);
+  auto block_of = [&](int64_t s) -> int32_t { return s >= 0 && s < num_slots ? (int32_t)(s >> 4) : -1; };
+  const int32_t b0 = block_of(raw0), b_prev = block_of(raw_prev), b1 = block_of(raw1), b2 = block_of(raw2);
+  if (reports && lane < run && raw0 >= num_slots) raise_device_error(PA_DEVERR_SLOT);
+
+  // leaders: the run's first entry of a block that none of the 31 entries before it names
+  const uint32_t same0 = __match_any_sync(kAll, b0);
+  uint32_t todo = __ballot_sync(kAll, b0 >= 0 && lane < run && (same0 & ((1u << lane) - 1u)) == 0);
+  const int32_t my_row = lane / kLanes;
+  const int32_t my_col = (lane % kLanes) * E;
+  while (todo) {
+    const int32_t first = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int32_t blk = __shfl_sync(kAll, b0, first);
+    if (__any_sync(kAll, b_prev == blk && lane > first)) continue;  // an earlier entry leads
+    // its entries: first .. first + 31; tokens of the block behind them are not written
+    const uint32_t in0 = __ballot_sync(kAll, b0 == blk), in1 = __ballot_sync(kAll, b1 == blk && lane < first);
+    if (__any_sync(kAll, (b1 == blk && lane >= first) || (b2 == blk && lane + 1 < first)) && reports && lane == 0)
       raise_device_error(PA_DEVERR_SLOT);
 
     uint8_t* tile = pool + (size_t)blk * lay.block_bytes + ((size_t)kv * num_kv_heads + h) * 16 * D;
     float* scale_at = reinterpret_cast<float*>(pool + q8_scale_at(lay, blk, kv, h, num_kv_heads));
     const float s_old = *scale_at;
 
-    // row -> entry of the window (0xff: not written now)
-    const bool member = blk_here == blk;
+    // row -> entry, counted from t0 (0xff: not written now); of a row's entries the latest
+    __syncwarp();
     if (lane < 16) row_src[warp][lane] = 0xff;
     __syncwarp();
-    const uint32_t same = __match_any_sync(0xffffffffu, member ? (int32_t)(s & 15) : 16 + lane);
-    if (member && (same >> lane) == 1u) row_src[warp][s & 15] = (uint8_t)lane;  // the latest of its row
-    __syncwarp();
-    const uint4 rs = *reinterpret_cast<const uint4*>(row_src[warp]);
-    const uint32_t rsw[4] = {rs.x, rs.y, rs.z, rs.w};
-    __syncwarp();
-
-    In x[16];
-    float amax = 0.f;
-    bool odd = false;  // a non-finite element
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const uint32_t e = (rsw[r >> 2] >> (8 * (r & 3))) & 0xffu;
-      if (e != 0xffu)
-        x[r] = *reinterpret_cast<const In*>(src + ((size_t)(t + e) * num_kv_heads + h) * D + lane * PER);
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      if (((rsw[r >> 2] >> (8 * (r & 3))) & 0xffu) == 0xffu) continue;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float a = fabsf(Elem<T>::to_f32(x[r].v[i]));
-        if (a <= FLT_MAX) amax = fmaxf(amax, a);
-        else odd = true;
+    {
+      const bool m0 = (in0 >> lane) & 1u, m1 = (in1 >> lane) & 1u;
+      const int32_t r0 = m0 ? (int32_t)(raw0 & 15) : 32 + lane, r1 = m1 ? (int32_t)(raw1 & 15) : 32 + lane;
+      const uint32_t eq0 = __match_any_sync(kAll, r0);
+      if (m0 && (eq0 >> lane) == 1u) row_src[warp][r0] = (uint8_t)lane;
+      __syncwarp();
+      if (in1) {
+        const uint32_t eq1 = __match_any_sync(kAll, r1);
+        if (m1 && (eq1 >> lane) == 1u) row_src[warp][r1] = (uint8_t)(32 + lane);
+        __syncwarp();
       }
     }
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    if (__any_sync(0xffffffffu, odd) && lane == 0) raise_device_error(PA_DEVERR_NONFINITE);
+    const bool fresh = row_src[warp][0] != 0xff;
+
+    Words x[kSteps];
+    uint32_t written = 0;  // bit i: this lane's row of step i is new
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t e = row_src[warp][i * kRows + my_row];
+      x[i].q = make_uint4(0, 0, 0, 0);
+      if (e != 0xffu) {
+        written |= 1u << i;
+        x[i].q = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(t0 + e) * num_kv_heads + h) * D + my_col));
+      }
+    }
+    // largest magnitude, on the bit patterns
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) top = Bits<T>::max_abs(top, x[i].w[c]);
+    top = __reduce_max_sync(kAll, Bits<T>::widest(top));
+    const bool odd = top >= 0x7f800000u;  // a NaN or an infinity among the rows
+    if (odd) {
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int c = 0; c < E; ++c) {
+          const uint32_t a = __float_as_uint(fabsf(x[i].get(c)));
+          if (a < 0x7f800000u) top = max(top, a);
+        }
+      top = __reduce_max_sync(kAll, top);
+      if (lane == 0) raise_device_error(PA_DEVERR_NONFINITE);
+    }
+    float amax = __uint_as_float(top);
     if (amax < kQ8Tiny) amax = 0.f;
-    const bool fresh = (rsw[0] & 0xffu) != 0xffu;
     const float s_new = fresh ? __fmul_rn(amax, Code::kInvMax) : Code::grown(s_old, amax);
     const float inv = s_new > 0.f ? __fdiv_rn(1.f, s_new) : 0.f;
 
     if (!fresh && s_new > s_old) {
       // rows that stay: coded again at the grown scale
       const float ratio = __fdiv_rn(s_old, s_new);
-      Codes c[16];
+      Codes c[kSteps];
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (((rsw[r >> 2] >> (8 * (r & 3))) & 0xffu) == 0xffu)
-          c[r] = *reinterpret_cast<const Codes*>(tile + r * D + lane * PER);
+      for (int i = 0; i < kSteps; ++i)
+        if (!((written >> i) & 1u)) c[i] = *reinterpret_cast<const Codes*>(tile + (i * kRows + my_row) * D + my_col);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (((rsw[r >> 2] >> (8 * (r & 3))) & 0xffu) != 0xffu) continue;
+      for (int i = 0; i < kSteps; ++i) {
+        if ((written >> i) & 1u) continue;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-          c[r].v[i] = (uint8_t)Code::encode(__fmul_rn(Code::decode(c[r].v[i]), ratio));
-        *reinterpret_cast<Codes*>(tile + r * D + lane * PER) = c[r];
+        for (int e = 0; e < E; ++e) c[i].v[e] = (uint8_t)Code::encode(__fmul_rn(Code::decode(c[i].v[e]), ratio));
+        *reinterpret_cast<Codes*>(tile + (i * kRows + my_row) * D + my_col) = c[i];
       }
     }
+    // the values are unpacked again here: kept since the maximum they would
+    // take twice the registers of the rows
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      if (((rsw[r >> 2] >> (8 * (r & 3))) & 0xffu) == 0xffu) continue;
-      Codes c;
+    for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        float y = Elem<T>::to_f32(x[r].v[i]);
-        if (!(fabsf(y) <= FLT_MAX)) y = y != y ? 0.f : copysignf(FLT_MAX, y);  // NaN -> 0, inf -> the largest code
-        c.v[i] = (uint8_t)Code::encode(__fmul_rn(y, inv));
+      for (int c = 0; c < 4; ++c) asm volatile("" : "+r"(x[i].w[c]));
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (!((written >> i) & 1u)) continue;
+      Vec<uint32_t, E / 4> c;
+      if (!odd) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          c.v[e / 4] = Code::encode4(__fmul_rn(x[i].get(e), inv), __fmul_rn(x[i].get(e + 1), inv),
+                                     __fmul_rn(x[i].get(e + 2), inv), __fmul_rn(x[i].get(e + 3), inv));
+      } else {
+        for (int e = 0; e < E / 4; ++e) c.v[e] = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float y = x[i].get(e);
+          if (!(fabsf(y) <= FLT_MAX)) y = y != y ? 0.f : copysignf(FLT_MAX, y);  // NaN -> 0, inf -> the largest code
+          c.v[e / 4] |= Code::encode(__fmul_rn(y, inv)) << (8 * (e % 4));
+        }
       }
-      *reinterpret_cast<Codes*>(tile + r * D + lane * PER) = c;
+      *reinterpret_cast<Vec<uint32_t, E / 4>*>(tile + (i * kRows + my_row) * D + my_col) = c;
     }
     if (lane == 0 && (fresh || s_new != s_old)) *scale_at = s_new;
   }
@@ -141,17 +200,17 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
 template <typename T, int D, typename Code>
 inline cudaError_t launch_append_q8(const void* k, const void* v, void* pool, const int64_t* slots,
                                     int32_t num_tokens, int32_t num_kv_heads, int32_t num_blocks, cudaStream_t st) {
-  // One token per warp while that keeps the warps to a few per SM (a decode
-  // step: every token leads a tile of its own); with more, a warp goes through
-  // up to 16 entries, of which a prompt's tokens make one or two tiles.
+  // One entry per warp while that keeps the warps to a few per SM (a decode
+  // step: every token leads a tile of its own); with more, a warp takes a run
+  // of entries, of which a prompt's tokens make one or two tiles.
   const int64_t tiles = (int64_t)num_tokens * num_kv_heads * 2;
-  int32_t per_warp = 1;
-  while (per_warp < 16 && tiles / per_warp > (int64_t)64 * device_sm_count()) per_warp *= 2;
-  const int64_t per_cta = (int64_t)per_warp * kAppendQ8Warps;
+  int32_t run = 1;
+  while (run < kAppendQ8Run && tiles / run > (int64_t)64 * device_sm_count()) run *= 2;
+  const int64_t per_cta = (int64_t)run * kAppendQ8Warps;
   const dim3 grid((unsigned)((num_tokens + per_cta - 1) / per_cta), (unsigned)num_kv_heads, 2);
   append_q8_kernel<T, D, Code><<<grid, kAppendQ8Warps * 32, 0, st>>>(
       reinterpret_cast<const T*>(k), reinterpret_cast<const T*>(v), reinterpret_cast<uint8_t*>(pool), slots,
-      num_tokens, num_kv_heads, (int64_t)num_blocks * 16, q8_layout(num_kv_heads, D), per_warp);
+      num_tokens, num_kv_heads, (int64_t)num_blocks * 16, q8_layout(num_kv_heads, D), run);
   return cudaGetLastError();
 }
 

@@ -51,6 +51,14 @@ struct CodeInt8 {
   __device__ __forceinline__ static uint32_t encode(float x) {
     return (uint32_t)max(-127, min(127, __float2int_rn(x))) & 0xffu;
   }
+  // Four codes of one word, of values within [-127.5, 127.5): adding 1.5 * 2^23
+  // rounds to the integer, ties to even, and leaves it in the low bits.
+  __device__ __forceinline__ static uint32_t encode4(float a, float b, float c, float d) {
+    const float big = 12582912.f;
+    const uint32_t ab = __byte_perm(__float_as_uint(__fadd_rn(a, big)), __float_as_uint(__fadd_rn(b, big)), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(__fadd_rn(c, big)), __float_as_uint(__fadd_rn(d, big)), 0x0040);
+    return __byte_perm(ab, cd, 0x5410);
+  }
   __device__ __forceinline__ static float decode(uint32_t c) { return (float)(int8_t)c; }
 };
 struct CodeE4m3 {
@@ -69,6 +77,12 @@ struct CodeE4m3 {
     uint16_t h;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(x));
     return h & 0xffu;
+  }
+  __device__ __forceinline__ static uint32_t encode4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | (uint32_t)hi << 16;
   }
   __device__ __forceinline__ static float decode(uint32_t c) {
     uint32_t h2;
