@@ -93,35 +93,42 @@ def rows_of(codes, scales, table, length: int, code: str) -> np.ndarray:
     return x.transpose(1, 2, 0, 3, 4).reshape(2, x.shape[2], -1, x.shape[4])[:, :, :length]
 
 
-def attention(q: np.ndarray, kv: np.ndarray, scale: float, v_scales: np.ndarray):
+def scale_rows(scales, table, length: int) -> np.ndarray:
+    """[2][Hkv][length] fp64: the K and V scale of each of a sequence's tokens."""
+    return scales[np.asarray(table[: (length + 15) // 16], np.int64)].astype(np.float64).repeat(16, 0)[:length].transpose(
+        1, 2, 0)
+
+
+def attention(q: np.ndarray, kv: np.ndarray, scale: float, scales: np.ndarray):
     """Causal attention of the last len(q) of kv's tokens: q fp64 [n][H][D], kv
-    fp64 [2][Hkv][L][D], v_scales [Hkv][L] each token's V scale. Returns out and
-    what bound() needs, each [n][H][D] or [n][H][1]: the sum of p |v|, the
-    largest scale * sum |q_d k_d| over the tokens seen, and the largest
-    p * v_scale times the sum of the |V codes|."""
+    fp64 [2][Hkv][L][D], scales [2][Hkv][L] from scale_rows. Returns out and what
+    bound() needs, each [n][H][D] or [n][H][1]:
+      mag   the sum of p |v|
+      big   the largest scale * sum |q_d k_d| over the tokens seen
+      low   the largest p * v_scale (a scale of 0 counts as 1) times the sum of
+            the |V codes|
+      big1  the largest scale * k_scale * sum |q_d|
+      mag1  the sum of p * v_scale"""
     n, H, D = q.shape
     G, L = H // kv.shape[1], kv.shape[2]
     out, mag, big, low = np.empty((n, H, D)), np.empty((n, H, D)), np.empty((n, H, 1)), np.empty((n, H, D))
+    big1, mag1 = np.empty((n, H, 1)), np.empty((n, H, 1))
     seen = np.arange(L) <= (L - n + np.arange(n))[:, None]
     for h in range(H):
-        k, v = kv[:, h // G]
-        vs = v_scales[h // G].astype(np.float64)
+        (k, v), (ks, vs) = kv[:, h // G], scales[:, h // G]
         s = np.where(seen, scale * (q[:, h] @ k.T), -np.inf)
         p = np.exp(s - s.max(1, keepdims=True))
         p /= p.sum(1, keepdims=True)
         out[:, h], mag[:, h] = p @ v, p @ np.abs(v)
         big[:, h, 0] = np.where(seen, abs(scale) * (np.abs(q[:, h]) @ np.abs(k).T), 0).max(1)
-        codes = np.abs(v) / np.where(vs > 0, vs, 1)[:, None]
-        low[:, h] = (p * vs).max(1, keepdims=True) * (seen @ codes)
-    return out, (mag, big, low)
+        big1[:, h, 0] = abs(scale) * np.abs(q[:, h]).sum(1) * np.where(seen, ks, 0).max(1)
+        mag1[:, h, 0] = p @ vs
+        vs = np.where(vs > 0, vs, 1)
+        low[:, h] = (p * vs).max(1, keepdims=True) * (seen @ (np.abs(v) / vs[:, None]))
+    return out, (mag, big, low, big1, mag1)
 
 
-def v_scale_rows(scales, table, length: int) -> np.ndarray:
-    """[Hkv][length]: the V scale of each of a sequence's tokens."""
-    return scales[np.asarray(table[: (length + 15) // 16], np.int64), 1].repeat(16, 0)[:length].T
-
-
-def bound(ref, terms, dim: int, length: int, io: str, p_rounding: float, p_floor: float) -> np.ndarray:
+def bound(ref, terms, dim: int, length: int, io: str, p_rounding: float, p_floor: float, biased: bool) -> np.ndarray:
     """What an output may be off by: the output's rounding, and of the sum of
     p |v| the rounding of each probability (p_rounding), the scores' errors
     (fp32 sums of dim terms; the exponent's argument passes a few roundings of
@@ -130,8 +137,17 @@ def bound(ref, terms, dim: int, length: int, io: str, p_rounding: float, p_floor
     p_floor: smallest spacing of the type that holds p * v_scale, relative to
     the largest of them: each such product may be off by half of it, whatever
     its own size, and multiplies a V code. fp16 products whose largest is at
-    least 2^7 lie on a grid of 2^-24 there: 2^-31."""
-    mag, big, low = terms
+    least 2^7 lie on a grid of 2^-24 there: 2^-31.
+    biased: the sums over codes are formed over code + 128 <= 255 and 128 times
+    the sum of the other factor is taken off, so their fp32 errors are relative
+    to 255 sum |q_d| k_scale and to 255 sum p v_scale in place of sum |q_d k_d|
+    and sum p |v|; the subtraction rounds once more at that size."""
+    mag, big, low, big1, mag1 = terms
+    if biased:
+        big, chain = 255 * big1, 255 * mag1
+    else:
+        chain = mag
     score = (dim + 16) * 2.0 ** -24 + (2.0 ** -22 if io == "f32" else 0.0)
-    eps = p_rounding + 2 * score * big + 16 * 2.0 ** -24 * big + 2.0 ** -20 + (length + 16) * 2.0 ** -24
-    return (2.0 ** -8 if io == "bf16" else 2.0 ** -23) * np.abs(ref) + eps * mag + p_floor / 2 * low + 1e-30
+    eps = p_rounding + 2 * score * big + 16 * 2.0 ** -24 * big + 2.0 ** -20
+    return ((2.0 ** -8 if io == "bf16" else 2.0 ** -23) * np.abs(ref) + eps * mag
+            + (length + 16) * 2.0 ** -24 * chain + p_floor / 2 * low + 1e-30)

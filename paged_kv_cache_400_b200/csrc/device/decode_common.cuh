@@ -66,9 +66,7 @@ __device__ __forceinline__ void grid_dependents_launch() {
 constexpr int kMergeThreads = 128;
 constexpr int kMergeMaxParts = 64;
 
-// kWaitFirst: every CTA waits for the partition kernel, also one that has
-// nothing to merge, so that this grid never completes before that one.
-template <typename T, int D, bool kWaitFirst = false>
+template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) partition_merge_kernel(DecodeParams p) {
   constexpr int kOut = 4;     // output elements per thread per round
   constexpr int kChunk = 16;  // partitions summed per round
@@ -79,9 +77,8 @@ __global__ void __launch_bounds__(kMergeThreads) partition_merge_kernel(DecodePa
   const int32_t G = p.group;
   const int32_t L = checked_len(p, b, false);
   const int32_t nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
-  if (kWaitFirst) grid_dependency_wait();
   if (nparts <= 1) return;  // finished by the partition kernel
-  if (!kWaitFirst) grid_dependency_wait();   // the partition kernel's states are complete and visible
+  grid_dependency_wait();   // the partition kernel's states are complete and visible
   const size_t bh0 = (size_t)b * p.num_heads + (size_t)g * G;
   if (nparts <= kMergeMaxParts) {
     for (int32_t i = threadIdx.x; i < G * nparts; i += blockDim.x) {
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(kMergeThreads) partition_merge_kernel(DecodePa
 
 // Launches partition_merge_kernel as a programmatic dependent of the kernel
 // just launched on `st` (which calls griddepcontrol.launch_dependents).
-template <typename T, int D, bool kWaitFirst = false>
+template <typename T, int D>
 inline cudaError_t launch_partition_merge(const DecodeParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_kv_heads, p.num_seqs);
@@ -168,7 +165,7 @@ inline cudaError_t launch_partition_merge(const DecodeParams& p, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, partition_merge_kernel<T, D, kWaitFirst>, p);
+  return cudaLaunchKernelEx(&cfg, partition_merge_kernel<T, D>, p);
 }
 
 }  // namespace pagedkv

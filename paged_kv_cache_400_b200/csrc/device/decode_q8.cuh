@@ -19,27 +19,38 @@
 //    tokens (V, transposed in 16-bit units). Unpacked in place these are the A
 //    fragments of a K axis (K) or M axis (V) in another order, and that order is
 //    undone where it is free: in the query fragments and in the output's rows.
-//    int8: two byte permutes put codes + 128 under the exponent of 1024, one
-//    fp16x2 subtraction leaves them exact (5 instructions per 4 codes); e4m3:
-//    the hardware conversion.
-//  * The reference a head's exponentials are taken against rises only when a
-//    score exceeds it by more than 2^8, which one warp vote finds out; the
+//    e4m3: the hardware conversion. int8, fp32 queries: two byte permutes put
+//    code + 128 under the exponent of 1024, one subtraction leaves the code.
+//    int8, bf16 queries: the subtraction is put off; the bytes code + 128 stand
+//    in fp16's subnormals, u 2^-24, and 128 times the sum of the queries, or of
+//    the probabilities (one more MMA, against ones), comes off the fp32 sums.
+//    That costs 8 bits of those sums' headroom, against 5 bits that bf16 and
+//    the fp16 probabilities leave unused, and saves a quarter of the block's
+//    instructions.
+//  * The reference a head's exponentials are taken against rises only when an
+//    exponent exceeds it by more than 8, which one warp vote finds out; the
 //    shuffles of a true running maximum are left out of the common block.
 //
-// Two references per head: m for the sum l = sum 2^(x - m), and n for what is
-// fed to the tensor core, P = 2^(x + log2 v_b - n + 7), whose largest value lies
-// in [2^7, 2^15] whatever the V scales are: fp16 holds P to 2^-11 relative down
-// to 2^-21 of the head's largest, and to 2^-32 of that largest below.
+// What the tensor core is fed is P = 2^(x + log2 v_b - n + 7) with x the score
+// and n the reference of the head: its largest value lies in [2^7, 2^15]
+// whatever the V scales are, so fp16 holds P to 2^-11 relative down to 2^-21 of
+// the head's largest, and to 2^-32 of that largest below. n is kept as the sum
+// of a score m and a log2 v_b, r: where scores are so large that fp32 spaces
+// them by more than a fraction, x - m is formed first, from rounded x, so that
+// the largest exponent is still what it should be. The same fp32 values of P,
+// before they are rounded, give the sum l += P / v_b. A V scale of 0 counts as
+// 1 there, and its block adds nothing to the output.
 //
 // fp32 queries: q (scaled per head by a power of two) and P are split into two
 // fp16 terms each (22 significand bits), each term its own MMA.
 //
-// Staging, work list and partitions are those of decode_staged.cuh: a ring of
+// Staging, work list and // Staging and work list are those of decode_staged.cuh:: a ring of
 // TMA boxes per warp (here one box of K and V per block), one CTA per
 // (partition, KV head, sequence) or, from kWorkListPartitions on, resident CTAs
-// that take them from the plan's list; partition_merge_kernel joins them.
+// that take them from the plan's list; a merge kernel joins them.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "decode_staged.cuh"
@@ -48,18 +59,21 @@
 namespace pagedkv {
 
 constexpr int kQ8Warps = 4;
-constexpr int kQ8RingBytes = 16384;  // per warp: 4 blocks of head_dim 128, 8 of 64
-constexpr int kQ8Smem = kQ8Warps * kQ8RingBytes + 1024;
-constexpr float kQ8Raise = 8.0f;     // a reference rises past this excess (log2)
+constexpr int kQ8Stages = 4;         // blocks in flight per warp
+constexpr float kQ8Raise = 8.0f;     // the reference rises past this excess (log2)
 constexpr float kQ8Lift = 7.0f;      // P is held 2^7 higher than its reference says: at most 2^15 in fp16
-constexpr float kQ8NoRef = -1e30f;   // reference n before any V scale was seen (finite: n - n stays 0)
+constexpr float kQ8Far = 1024.0f;    // scores (log2) from which fp32 leaves exponents less than 13 bits
+constexpr float kQ8NoRef = -3e38f;   // reference before any score was seen (finite: n - n stays 0)
 
 template <int D>
 struct Q8Tile {
   static constexpr int kLines = 16 * D / 128;        // 128-byte lines of a K or V tile
   static constexpr int kBytes = 16 * D;              // a K or V tile
   static constexpr int kStage = 2 * kBytes;
-  static constexpr int kStages = kQ8RingBytes / kStage;
+  static constexpr int kStages = kQ8Stages;
+  static constexpr int kRing = kStages * kStage;     // per warp
+  static constexpr int kSmem = kQ8Warps * kRing + 1024;
+  static constexpr int kCtasPerSm = D == 128 ? 3 : 5;  // by shared memory, and by registers for groups of up to 8 heads
   // Byte offset of 16-byte chunk c of token t in a tile, 128-byte swizzle: the
   // chunk's place in its line is XORed with the line's index, so the 8 rows of
   // an ldmatrix fall in 8 different bank groups for both head sizes.
@@ -71,7 +85,7 @@ struct Q8Tile {
 };
 
 struct Q8Shared {
-  uint64_t bars[kQ8Warps][8];
+  uint64_t bars[kQ8Warps][kQ8Stages];
   float red_m[kQ8Warps][16];
   float red_l[kQ8Warps][16];
   int32_t next_item;
@@ -93,6 +107,13 @@ __device__ __forceinline__ void q8_unpack(CodeE4m3, uint32_t w, bool interleaved
       "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
       : "=r"(p), "=r"(q)
       : "r"(w));
+}
+
+// The same word as four fp16 subnormals (code + 128) 2^-24.
+__device__ __forceinline__ void q8_unpack_biased(uint32_t w, bool interleaved, uint32_t& p, uint32_t& q) {
+  const uint32_t u = w ^ 0x80808080u;
+  p = __byte_perm(u, 0, interleaved ? 0x4240 : 0x4140);
+  q = __byte_perm(u, 0, interleaved ? 0x4341 : 0x4342);
 }
 
 // D = A * B + D, A 16x16 fp16 (row), B 16x8 fp16 (col), D 16x8 fp32.
@@ -121,6 +142,16 @@ __device__ __forceinline__ uint32_t pack_f16x2_rest(float lo, float hi, uint32_t
   return pack_f16x2(lo - __low2float(h), hi - __high2float(h));
 }
 
+// Read through L2 (written by another SM just before).
+__device__ __forceinline__ Vec<float, 4> load_cg(const Vec<float, 4>* a) {
+  const float4 x = __ldcg(reinterpret_cast<const float4*>(a));
+  return {{x.x, x.y, x.z, x.w}};
+}
+__device__ __forceinline__ Vec<float, 2> load_cg(const Vec<float, 2>* a) {
+  const float2 x = __ldcg(reinterpret_cast<const float2*>(a));
+  return {{x.x, x.y}};
+}
+
 __device__ __forceinline__ float ex2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -128,18 +159,27 @@ __device__ __forceinline__ float ex2_ftz(float x) {
 }
 
 // Attention over partition `part` of sequence b for KV head g (all G query
-// heads, NT = ceil(G / 8) tiles of 8). `phase` as in decode_partition.
-template <typename T, int D, int NT, typename Code>
+// heads, NT = ceil(G / 8) tiles of 8), by W warps: a CTA (4), or one warp on its
+// own (then part 0, the whole sequence). `phase` as in decode_partition.
+template <typename T, int D, int NT, typename Code, int W>
 __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, const DecodeParams& p,
-                                                    const Q8Layout& lay, uint8_t* smem, Q8Shared& sh, int32_t part,
-                                                    int32_t g, int32_t b, int32_t L, uint32_t& phase) {
+                                                    const Q8Layout& lay, uint8_t* smem, int32_t ring_bytes,
+                                                    Q8Shared& sh, int32_t part, int32_t g, int32_t b, int32_t L,
+                                                    uint32_t& phase) {
   using Tile = Q8Tile<D>;
   constexpr int S = Tile::kStages;
   constexpr int KK = D / 16;                              // k-steps of QK, row tiles of PV
   constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;           // fp16 terms of q and P
+  constexpr bool kBias = std::is_same<Code, CodeInt8>::value && TERMS == 1;  // codes as (c + 128) 2^-24
+  constexpr float kUnit = kBias ? 16777216.f : 1.f;       // what an operand of the MMAs has to be multiplied by
+  auto unpack = [](uint32_t w, bool interleaved, uint32_t& lo, uint32_t& hi) {
+    if constexpr (kBias) q8_unpack_biased(w, interleaved, lo, hi);
+    else q8_unpack(Code{}, w, interleaved, lo, hi);
+  };
   constexpr int kRow = D + 8;                             // floats per row of the merge buffer
-  static_assert(kQ8Warps * 8 * NT * kRow * 4 <= kQ8Warps * kQ8RingBytes, "the merge buffer reuses the stages");
+  static_assert(8 * NT * kRow * 4 <= Tile::kRing, "the merge buffer reuses the stages");
   const int32_t warp = threadIdx.x >> 5;
+  const int32_t rank = W == 1 ? 0 : warp;  // of the W warps: owns blocks rank, rank + W, ...
   const int32_t lane = threadIdx.x & 31;
   const int32_t gid = lane >> 2;
   const int32_t tig = lane & 3;
@@ -151,13 +191,14 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   const int32_t t0 = part * PT;
   const int32_t t1 = min(t0 + PT, L);
   const int32_t nb = (t1 - t0 + 15) >> 4;
-  const int32_t my = nb > warp ? (nb - warp + kQ8Warps - 1) / kQ8Warps : 0;
-  uint8_t* wsm = smem + warp * kQ8RingBytes;
+  const int32_t my = nb > rank ? (nb - rank + W - 1) / W : 0;
+  uint8_t* wsm = smem + warp * ring_bytes;
   const uint32_t wsm_addr = smem_addr(wsm);
   const int32_t* table = p.block_tables + (size_t)b * p.max_blocks + (t0 >> 4);
 
-  // lane i holds the id of the warp's i-th block and, once they arrive, its scales
-  const int32_t my_blk = lane < my ? __ldg(table + warp + lane * kQ8Warps) : -1;
+  // lane i holds the id of the warp's i-th block and, once they arrive, its
+  // scales: k_b, log2 v_b and 1 / v_b
+  const int32_t my_blk = lane < my ? __ldg(table + rank + lane * W) : -1;
   const bool my_ok = my_blk >= 0 && my_blk < p.num_blocks;
   if (lane < my && !my_ok) raise_device_error(PA_DEVERR_BLOCK);
   const uint32_t ok_mask = __ballot_sync(0xffffffffu, my_ok);
@@ -179,17 +220,25 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   const int32_t npre = my < S ? my : S;
   for (int32_t i = 0; i < npre; ++i) issue(i);
 
-  float my_ks = 0.f, my_lv = 0.f;  // K scale; log2 of the V scale
+  float my_ks = 0.f, my_lv = 0.f, my_rv = 1.f;
+  bool has_v = false;
   if (my_ok) {
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.pool);
     my_ks = __ldg(reinterpret_cast<const float*>(pool + q8_scale_at(lay, my_blk, 0, g, p.num_kv_heads)));
-    my_lv = log2f(__ldg(reinterpret_cast<const float*>(pool + q8_scale_at(lay, my_blk, 1, g, p.num_kv_heads))));
+    const float vs = __ldg(reinterpret_cast<const float*>(pool + q8_scale_at(lay, my_blk, 1, g, p.num_kv_heads)));
+    has_v = vs > 0.f;
+    if (has_v) {
+      my_lv = log2f(vs);
+      my_rv = 1.f / vs;
+    }
   }
+  const uint32_t v_mask = __ballot_sync(0xffffffffu, has_v);
 
   // Query fragments: B of S^T = K Q^T, head 8 nt + gid, dims 16 kk + 4 tig + (0, 1 | 2, 3),
   // scaled per head so that its largest magnitude lies in [2^14, 2^15).
   uint32_t qb[TERMS][NT][KK][2];
-  float sfac[NT][2];  // scale * log2 e / that power of two, heads 8 nt + 2 tig (+ 1)
+  float sfac[NT][2];  // scale * log2 e * unit / that power of two, heads 8 nt + 2 tig (+ 1)
+  float qsum[NT][2];  // 128 / unit * the sum of the scaled query (kBias)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int32_t head = 8 * nt + gid;
@@ -221,23 +270,43 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
         if constexpr (TERMS == 2) qb[1][nt][kk][j] = pack_f16x2_rest(lo, hi, qb[0][nt][kk][j]);
       }
     }
-    sfac[nt][0] = __shfl_sync(0xffffffffu, down, 8 * tig);
-    sfac[nt][1] = __shfl_sync(0xffffffffu, down, 8 * tig + 4);
+    sfac[nt][0] = __shfl_sync(0xffffffffu, down, 8 * tig) * kUnit;
+    sfac[nt][1] = __shfl_sync(0xffffffffu, down, 8 * tig + 4) * kUnit;
+    if constexpr (kBias) {
+      float sum = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 x2 = __half22float2(*reinterpret_cast<const __half2*>(&qb[0][nt][kk][j]));
+          sum += x2.x + x2.y;
+        }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qsum[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * tig) * (128.f / kUnit);
+      qsum[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4) * (128.f / kUnit);
+    } else {
+      qsum[nt][0] = qsum[nt][1] = 0.f;
+    }
   }
 
   float o[KK][NT][4];
-  float m[NT][2], n[NT][2], l[NT][2];
+  float ps[NT][4];                     // kBias: the sums of the P that o is made of
+  float m[NT][2], r[NT][2], l[NT][2];  // reference m + r and sum, heads 8 nt + 2 tig (+ 1); o, l in units of 2^(m + r - lift)
+  bool far = false;                    // some |m| > kQ8Far (the same in the whole warp)
+  auto clear = [&]() {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kQ8NoRef;
+      r[nt][0] = r[nt][1] = l[nt][0] = l[nt][1] = 0.f;
+      ps[nt][0] = ps[nt][1] = ps[nt][2] = ps[nt][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      m[nt][j] = -INFINITY;
-      n[nt][j] = kQ8NoRef;
-      l[nt][j] = 0.f;
+      for (int c = 0; c < KK; ++c) o[c][nt][0] = o[c][nt][1] = o[c][nt][2] = o[c][nt][3] = 0.f;
     }
-#pragma unroll
-    for (int c = 0; c < KK; ++c) o[c][nt][0] = o[c][nt][1] = o[c][nt][2] = o[c][nt][3] = 0.f;
-  }
+  };
+  clear();
+  const int32_t row = lane & 15;  // of this lane's ldmatrix address
+  const uint32_t row_addr = wsm_addr + Tile::chunk(row, lane >> 4);
 
   for (int32_t i = 0; i < my; ++i) {
     const int32_t s = i % S;
@@ -251,109 +320,142 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
         mbar_wait_bounded(&sh.bars[warp][sk], (phase >> sk) & 1u, kWaitLimitNs);
         phase ^= 1u << sk;
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KK; ++c) o[c][nt][0] = o[c][nt][1] = o[c][nt][2] = o[c][nt][3] = 0.f;
-      }
+      clear();
       if (lane == 0) sh.abort = 1;
       break;
     }
     phase ^= 1u << s;
-    const int32_t nvalid = min(16, t1 - (t0 + (warp + i * kQ8Warps) * 16));
-    const bool valid = (ok_mask >> i) & 1u;
-    uint8_t* stg = wsm + s * Tile::kStage;
-    const uint32_t st = wsm_addr + s * Tile::kStage;
+    const int32_t nvalid = min(16, t1 - (t0 + (rank + i * W) * 16));
     const float ks = __shfl_sync(0xffffffffu, my_ks, i);
     const float lv = __shfl_sync(0xffffffffu, my_lv, i);
-    if constexpr (std::is_same<Code, CodeE4m3>::value) {
-      // rows behind the sequence end may hold NaN codes, which a zero
-      // probability does not silence: their V rows become zero
-      if (valid && nvalid < 16) {
-        for (int32_t e = lane; e < (16 - nvalid) * (D / 16); e += 32)
-          *reinterpret_cast<uint4*>(stg + Tile::kBytes + Tile::chunk(nvalid + e / (D / 16), e % (D / 16))) =
-              make_uint4(0, 0, 0, 0);
-        __syncwarp();
+    const float rv = __shfl_sync(0xffffffffu, my_rv, i);
+    if (nvalid < 16 || !((v_mask >> i) & 1u)) {
+      // What must not count becomes zero codes: both tiles of a block that was
+      // not loaded, the V tile under a zero scale, and the V rows behind the
+      // sequence's end (they may hold NaN codes, which a zero probability does
+      // not silence).
+      uint8_t* stg = wsm + s * Tile::kStage;
+      const bool loaded = (ok_mask >> i) & 1u;
+      const int32_t from = (v_mask >> i) & 1u ? nvalid : 0;
+      for (int32_t e = lane; e < Tile::kStage / 16; e += 32) {
+        const int32_t kv = e / (Tile::kBytes / 16), t = e / (D / 16) % 16, c = e % (D / 16);
+        if (!loaded || (kv == 1 && t >= from))
+          *reinterpret_cast<uint4*>(stg + kv * Tile::kBytes + Tile::chunk(t, c)) = make_uint4(0, 0, 0, 0);
       }
+      __syncwarp();
     }
 
     // S^T: rows = tokens (gid, gid + 8), columns = heads (2 tig, 2 tig + 1)
-    float sc[NT][4];
+    const uint32_t at = row_addr + s * Tile::kStage;
+    float sc[NT][4], sc2[NT][4];  // even and odd k-steps: two shorter chains of dependent MMAs
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-    const int32_t tok = (lane & 7) + (((lane >> 3) & 1) << 3);
-    if (valid) {
-      float sc2[NT][4];  // odd k-steps: two shorter chains of dependent MMAs
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc2[nt][0] = sc2[nt][1] = sc2[nt][2] = sc2[nt][3] = 0.f;
+      for (int e = 0; e < 4; ++e) sc[nt][e] = sc2[nt][e] = 0.f;
 #pragma unroll
-      for (int c = 0; c < KK; c += 2) {
-        uint32_t r[4];
-        ldsm_x4(st + Tile::chunk(tok, c + (lane >> 4)), r[0], r[1], r[2], r[3]);
-        uint32_t a0[4], a1[4];
-        q8_unpack(Code{}, r[0], false, a0[0], a0[2]);
-        q8_unpack(Code{}, r[1], false, a0[1], a0[3]);
-        q8_unpack(Code{}, r[2], false, a1[0], a1[2]);
-        q8_unpack(Code{}, r[3], false, a1[1], a1[3]);
+    for (int c = 0; c < KK; c += 2) {
+      uint32_t w[4];
+      ldsm_x4(at ^ (c << 4), w[0], w[1], w[2], w[3]);
+      uint32_t a0[4], a1[4];
+      unpack(w[0], false, a0[0], a0[2]);
+      unpack(w[1], false, a0[1], a0[3]);
+      unpack(w[2], false, a1[0], a1[2]);
+      unpack(w[3], false, a1[1], a1[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int term = 0; term < TERMS; ++term) {
-            mma_f16_16816(sc[nt], a0, qb[term][nt][c][0], qb[term][nt][c][1]);
-            mma_f16_16816(sc2[nt], a1, qb[term][nt][c + 1][0], qb[term][nt][c + 1][1]);
-          }
+        for (int term = 0; term < TERMS; ++term) {
+          mma_f16_16816(sc[nt], a0, qb[term][nt][c][0], qb[term][nt][c][1]);
+          mma_f16_16816(sc2[nt], a1, qb[term][nt][c + 1][0], qb[term][nt][c + 1][1]);
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] += sc2[nt][e];
     }
-    bool exceeds = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int32_t row = gid + (e >> 1) * 8;
-        const float x = row < nvalid ? sc[nt][e] * (sfac[nt][e & 1] * ks) : -INFINITY;
-        sc[nt][e] = x;
-        exceeds |= x > m[nt][e & 1] + kQ8Raise || x + lv > n[nt][e & 1] + kQ8Raise;
-      }
-    }
-    if (__any_sync(0xffffffffu, exceeds)) {
-      // both references to the largest score so far
+      for (int e = 0; e < 4; ++e) sc[nt][e] += sc2[nt][e];
+    // the exponents x + log2 v_b - (m + r) + lift
+    float x[NT][4];
+    auto exponents = [&]() {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float bm = fmaxf(sc[nt][j], sc[nt][j + 2]);
-          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-          const float mn = fmaxf(m[nt][j], bm), nn = fmaxf(n[nt][j], bm + lv);
-          const float am = ex2_ftz(m[nt][j] - mn), an = ex2_ftz(n[nt][j] - nn);
-          m[nt][j] = mn;
-          n[nt][j] = nn;
-          l[nt][j] *= am;
-#pragma unroll
-          for (int c = 0; c < KK; ++c) {
-            o[c][nt][j] *= an;
-            o[c][nt][j + 2] *= an;
+          const float f = sfac[nt][j] * ks, c = lv + kQ8Lift - r[nt][j];
+          if (!far) {
+            const float c2 = kBias ? fmaf(-qsum[nt][j], f, c - m[nt][j]) : c - m[nt][j];
+            x[nt][j] = fmaf(sc[nt][j], f, c2);
+            x[nt][j + 2] = fmaf(sc[nt][j + 2], f, c2);
+          } else {
+            x[nt][j] = (__fmul_rn(sc[nt][j] - qsum[nt][j], f) - m[nt][j]) + c;
+            x[nt][j + 2] = (__fmul_rn(sc[nt][j + 2] - qsum[nt][j], f) - m[nt][j]) + c;
           }
         }
       }
+      if (nvalid < 16) {  // rows behind the end
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (gid + (e >> 1) * 8 >= nvalid) x[nt][e] = -INFINITY;
+      }
+    };
+    exponents();
+    float top = x[0][0];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, x[nt][e]);
+    if (__any_sync(0xffffffffu, top > kQ8Lift + kQ8Raise)) {
+      // the reference to the largest x + log2 v_b so far
+      bool now_far = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float bm = m[nt][j], br = r[nt][j];
+#pragma unroll
+          for (int e = j; e < 4; e += 2) {
+            const float y = __fmul_rn(sc[nt][e] - qsum[nt][j], sfac[nt][j] * ks);
+            if (gid + (e >> 1) * 8 < nvalid && y + lv > bm + br) {
+              bm = y;
+              br = lv;
+            }
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, bm, off), orr = __shfl_xor_sync(0xffffffffu, br, off);
+            // one order for both lanes of a pair, so that all end with the same reference
+            if (om + orr > bm + br || (om + orr == bm + br && om > bm)) {
+              bm = om;
+              br = orr;
+            }
+          }
+          const float a = ex2_ftz((m[nt][j] - bm) + (r[nt][j] - br));
+          m[nt][j] = bm;
+          r[nt][j] = br;
+          now_far |= fabsf(bm) > kQ8Far && bm != kQ8NoRef;
+          l[nt][j] *= a;
+          ps[nt][j] *= a;
+          ps[nt][j + 2] *= a;
+#pragma unroll
+          for (int c = 0; c < KK; ++c) {
+            o[c][nt][j] *= a;
+            o[c][nt][j + 2] *= a;
+          }
+        }
+      }
+      far = __any_sync(0xffffffffu, now_far);
+      exponents();
     }
     uint32_t pb[TERMS][NT][2];  // B of O^T = V^T P^T: head gid, tokens 2 tig (+ 1), + 8
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float pv[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pv[e] = ex2_ftz(sc[nt][e] + (lv + kQ8Lift - n[nt][e & 1]));
+      for (int e = 0; e < 4; ++e) pv[e] = ex2_ftz(x[nt][e]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        l[nt][j] += ex2_ftz(sc[nt][j] - m[nt][j]) + ex2_ftz(sc[nt][j + 2] - m[nt][j]);
+      for (int j = 0; j < 2; ++j) l[nt][j] = fmaf(pv[j] + pv[j + 2], rv, l[nt][j]);
       const uint32_t w0 = pack_f16x2(pv[0], pv[1]), w1 = pack_f16x2(pv[2], pv[3]);
       pb[0][nt][0] = transpose_8x8(w0);
       pb[0][nt][1] = transpose_8x8(w1);
@@ -361,29 +463,64 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
         pb[1][nt][0] = transpose_8x8(pack_f16x2_rest(pv[0], pv[1], w0));
         pb[1][nt][1] = transpose_8x8(pack_f16x2_rest(pv[2], pv[3], w1));
       }
+      if constexpr (kBias) {
+        constexpr uint32_t one = 0x3c003c00u;
+        const uint32_t ones[4] = {one, one, one, one};
+        mma_f16_16816(ps[nt], ones, pb[0][nt][0], pb[0][nt][1]);
+      }
     }
-    if (valid) {
 #pragma unroll
-      for (int c = 0; c < KK; c += 2) {
-        uint32_t r[4];
-        ldsm_x4_trans(st + Tile::kBytes + Tile::chunk(tok, c + (lane >> 4)), r[0], r[1], r[2], r[3]);
-        uint32_t a0[4], a1[4];
-        q8_unpack(Code{}, r[0], true, a0[0], a0[1]);
-        q8_unpack(Code{}, r[1], true, a0[2], a0[3]);
-        q8_unpack(Code{}, r[2], true, a1[0], a1[1]);
-        q8_unpack(Code{}, r[3], true, a1[2], a1[3]);
+    for (int c = 0; c < KK; c += 2) {
+      uint32_t w[4];
+      ldsm_x4_trans((at ^ (c << 4)) + Tile::kBytes, w[0], w[1], w[2], w[3]);
+      uint32_t a0[4], a1[4];
+      unpack(w[0], true, a0[0], a0[1]);
+      unpack(w[1], true, a0[2], a0[3]);
+      unpack(w[2], true, a1[0], a1[1]);
+      unpack(w[3], true, a1[2], a1[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int term = 0; term < TERMS; ++term) {
-            mma_f16_16816(o[c][nt], a0, pb[term][nt][0], pb[term][nt][1]);
-            mma_f16_16816(o[c + 1][nt], a1, pb[term][nt][0], pb[term][nt][1]);
-          }
+        for (int term = 0; term < TERMS; ++term) {
+          mma_f16_16816(o[c][nt], a0, pb[term][nt][0], pb[term][nt][1]);
+          mma_f16_16816(o[c + 1][nt], a1, pb[term][nt][0], pb[term][nt][1]);
         }
       }
     }
     __syncwarp();
     if (i + S < my) issue(i + S);
+  }
+  if constexpr (kBias) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < KK; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][nt][e] = fmaf(o[c][nt][e], kUnit, -128.f * ps[nt][e]);
+  }
+
+  if constexpr (W == 1) {
+    // a head's sum lies in the 8 lanes of its column; dims 16 c + 2 gid (+ 1) here
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float ls = l[nt][j];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+        const int32_t head = 8 * nt + 2 * tig + j;
+        const float inv = 1.f / ls;
+        if (head < G) {
+          T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * H + (size_t)g * G + head) * D + 2 * gid;
+#pragma unroll
+          for (int c = 0; c < KK; ++c)
+            *reinterpret_cast<Vec<T, 2>*>(out + 16 * c) = {Elem<T>::from_f32(o[c][nt][j] * inv),
+                                                           Elem<T>::from_f32(o[c][nt][j + 2] * inv)};
+        }
+      }
+    }
+    return;
   }
 
   // ---- merge of the four warps' states -----------------------------------------
@@ -399,15 +536,13 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
       ls += __shfl_xor_sync(0xffffffffu, ls, 16);
       const int32_t head = 8 * nt + 2 * tig + j;
       if (gid == 0) {
-        sh.red_m[warp][head] = m[nt][j];
+        sh.red_m[warp][head] = m[nt][j] + r[nt][j];
         sh.red_l[warp][head] = ls;
       }
-      // the accumulators in units of 2^m, like l (a warp without blocks holds zeros)
-      const float f = m[nt][j] > -INFINITY ? exp2f(n[nt][j] - kQ8Lift - m[nt][j]) : 0.f;
       float* row = so + (warp * 8 * NT + head) * kRow + 2 * gid;
 #pragma unroll
       for (int c = 0; c < KK; ++c)
-        *reinterpret_cast<float2*>(row + 16 * c) = make_float2(o[c][nt][j] * f, o[c][nt][j + 2] * f);
+        *reinterpret_cast<float2*>(row + 16 * c) = make_float2(o[c][nt][j], o[c][nt][j + 2]);
     }
   }
   __syncthreads();
@@ -416,7 +551,7 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   for (int32_t i = threadIdx.x; i < G * D; i += blockDim.x) {
     const int32_t h = i / D;
     const int32_t d = i % D;
-    float M = -INFINITY;
+    float M = kQ8NoRef;
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sh.red_m[w][h]);
     float Ls = 0.f, A = 0.f;
@@ -440,7 +575,7 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
 }
 
 template <typename T, int D, int NT, typename Code>
-__global__ void __launch_bounds__(kQ8Warps * 32)
+__global__ void __launch_bounds__(kQ8Warps * 32, NT == 2 && sizeof(T) == 2 && D == 128 ? 3 : 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Layout lay) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Q8Shared sh;
@@ -471,7 +606,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
   __syncwarp();
   uint32_t phase = 0;
   if (p.work_items == nullptr) {
-    decode_q8_partition<T, D, NT, Code>(tmap, p, lay, smem, sh, blockIdx.x, blockIdx.y, blockIdx.z, grid_len, phase);
+    decode_q8_partition<T, D, NT, Code, kQ8Warps>(tmap, p, lay, smem, Q8Tile<D>::kRing, sh, blockIdx.x, blockIdx.y,
+                                                  blockIdx.z, grid_len, phase);
     return;
   }
   grid_dependency_wait();  // the plan kernel's item list is complete
@@ -488,8 +624,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
     const uint32_t bp = (uint32_t)__ldcg(p.work_items + item / p.num_kv_heads);
     const int32_t g = item % p.num_kv_heads;
     const int32_t b = (int32_t)(bp >> 16);
-    decode_q8_partition<T, D, NT, Code>(tmap, p, lay, smem, sh, (int32_t)(bp & 0xffffu), g, b,
-                                        checked_len(p, b, false), phase);
+    decode_q8_partition<T, D, NT, Code, kQ8Warps>(tmap, p, lay, smem, Q8Tile<D>::kRing, sh, (int32_t)(bp & 0xffffu), g, b,
+                                                  checked_len(p, b, false), phase);
     fence_proxy_async_smem();  // the item's shared-memory reads precede the next item's TMA writes
     if (threadIdx.x == 0) sh.next_item = next;
     __syncthreads();
@@ -497,7 +633,172 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
   }
 }
 
+// A warp per (sequence, KV head), for sequences of at most kQ8WarpTokens.
+constexpr int kQ8WarpTokens = 32 * 16;  // a lane holds one block id
+
+template <typename T, int D, int NT, typename Code>
+__global__ void __launch_bounds__(kQ8Warps * 32, NT == 2 && sizeof(T) == 2 && D == 128 ? 3 : 1)
+decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Layout lay, int32_t ring_bytes) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Q8Shared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int32_t warp = threadIdx.x >> 5;
+  const int32_t lane = threadIdx.x & 31;
+  grid_dependents_launch();
+  const int64_t item = (int64_t)blockIdx.x * kQ8Warps + warp;
+  if (item >= (int64_t)p.num_seqs * p.num_kv_heads) return;
+  const int32_t b = (int32_t)(item / p.num_kv_heads), g = (int32_t)(item % p.num_kv_heads);
+  const int32_t L = checked_len(p, b, g == 0 && lane == 0);
+  if (L == 0) {
+    T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_heads + (size_t)g * p.group) * D;
+    for (int32_t i = lane; i < p.group * D; i += 32) out[i] = Elem<T>::from_f32(0.f);
+    return;
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < Q8Tile<D>::kStages; ++s) mbar_init(&sh.bars[warp][s], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  uint32_t phase = 0;
+  decode_q8_partition<T, D, NT, Code, 1>(tmap, p, lay, smem, ring_bytes, sh, 0, g, b, L, phase);
+}
+
+// Merge of the partition states of one sequence: 4 warps per CTA, grid (H /
+// kHeads, B). kHeads > 1: a warp takes a head at a time (few partitions, or
+// few CTAs would have anything to do). kHeads == 1: the warps share a head's
+// partitions and join through shared memory. Bound by the latency of a few
+// dependent L2 reads: a warp has 8 partitions' accumulators in flight. Every
+// CTA waits for the partition kernel first, also one with nothing to merge, so
+// that this grid never completes before that one.
+constexpr int kQ8MergeWarps = 4;
+
+template <typename T, int D, bool kSplit>
+__global__ void __launch_bounds__(kQ8MergeWarps * 32) decode_q8_merge_kernel(DecodeParams p) {
+  constexpr int E = D / 32;  // output elements per lane
+  using Acc = Vec<float, E>;
+  __shared__ float sh_ml[kQ8MergeWarps][2];
+  __shared__ Acc sh_acc[kSplit ? kQ8MergeWarps : 1][32];
+  const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t b = blockIdx.y;
+  const int32_t L = checked_len(p, b, false);
+  const int32_t nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
+  grid_dependency_wait();
+  if (nparts <= 1) return;  // finished by the partition kernel
+  const int32_t heads = kSplit ? 1 : p.group;
+  for (int32_t h = kSplit ? 0 : warp; h < heads; h += kSplit ? 1 : kQ8MergeWarps) {
+    const size_t bh = (size_t)b * p.num_heads + (size_t)blockIdx.x * heads + h;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + bh * p.max_partitions;
+    const Acc* acc = reinterpret_cast<const Acc*>(p.ws_acc) + bh * p.max_partitions * 32 + lane;
+    // chunks of 32 partitions, this warp's first and the stride to its next
+    const int32_t c0 = kSplit ? warp * 32 : 0, step = kSplit ? kQ8MergeWarps * 32 : 32;
+    float M = kQ8NoRef, l = 0.f;
+    Acc a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.v[e] = 0.f;
+    for (int32_t q0 = c0; q0 < nparts; q0 += step) {
+      const int32_t cnt = min(32, nparts - q0);
+      const float2 s = lane < cnt ? __ldcg(ml + q0 + lane) : make_float2(kQ8NoRef, 0.f);
+      float m = s.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = fmaxf(m, M);
+      const float w = exp2f(s.x - m), old = exp2f(M - m);
+      M = m;
+      l = fmaf(l, old, warp_sum(s.y * w));
+#pragma unroll
+      for (int e = 0; e < E; ++e) a.v[e] *= old;
+      for (int32_t q = 0; q < cnt; q += 8) {
+        Acc x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q + j < cnt) x[j] = load_cg(acc + (size_t)(q0 + q + j) * 32);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, (q + j) & 31);
+          if (q + j < cnt) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) a.v[e] = fmaf(x[j].v[e], wj, a.v[e]);
+          }
+        }
+      }
+    }
+    if constexpr (kSplit) {
+      sh_acc[warp][lane] = a;
+      if (lane == 0) {
+        sh_ml[warp][0] = M;
+        sh_ml[warp][1] = l;
+      }
+      __syncthreads();
+      if (warp > 0) return;
+#pragma unroll
+      for (int w = 1; w < kQ8MergeWarps; ++w) {
+        const float m = fmaxf(M, sh_ml[w][0]);
+        const float f0 = exp2f(M - m), f1 = exp2f(sh_ml[w][0] - m);
+        M = m;
+        l = fmaf(l, f0, sh_ml[w][1] * f1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a.v[e] = fmaf(a.v[e], f0, sh_acc[w][lane].v[e] * f1);
+      }
+    }
+    const float inv = 1.f / l;
+    Vec<T, E> y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y.v[e] = Elem<T>::from_f32(a.v[e] * inv);
+    reinterpret_cast<Vec<T, E>*>(p.out)[bh * 32 + lane] = y;
+  }
+}
+
 // ---- host side ---------------------------------------------------------------
+
+template <typename T, int D, bool kSplit>
+inline cudaError_t launch_decode_q8_merge(const DecodeParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSplit ? p.num_heads : p.num_kv_heads, p.num_seqs);
+  cfg.blockDim = dim3(kQ8MergeWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_q8_merge_kernel<T, D, kSplit>, p);
+}
+
+// Tokens of a partition, a multiple of 16 in [128, 2048]: the resident CTAs
+// (q8_resident) take kQ8Rounds partitions each, or the smallest
+// multiple of that with which 2048 tokens are enough, when every sequence has
+// the longest length.
+#ifndef PA_Q8_ROUNDS
+#define PA_Q8_ROUNDS 1
+#endif
+constexpr int kQ8Rounds = PA_Q8_ROUNDS;
+#ifndef PA_Q8_WARP_PAIRS
+#define PA_Q8_WARP_PAIRS 3
+#endif
+inline int32_t q8_resident(int32_t head_dim) {
+  return (head_dim == 128 ? Q8Tile<128>::kCtasPerSm : Q8Tile<64>::kCtasPerSm) * device_sm_count();
+}
+inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
+  return max_seq_len <= kQ8WarpTokens && pairs >= (int64_t)PA_Q8_WARP_PAIRS * device_sm_count();
+}
+inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
+  const int64_t pairs = std::max<int64_t>((int64_t)num_seqs * num_kv_heads, 1);
+  if (q8_by_warp(pairs, max_seq_len)) return kQ8WarpTokens;  // one partition
+  const int64_t resident = (int64_t)q8_resident(head_dim) * kQ8Rounds;
+  const int64_t least = ((int64_t)max_seq_len + 2047) / 2048;  // partitions a sequence needs
+  const int64_t rounds = std::max<int64_t>((least * pairs + resident - 1) / resident, 1);
+  const int64_t parts = std::max<int64_t>(rounds * resident / pairs, 1);
+  const int64_t tokens = (((int64_t)max_seq_len + parts - 1) / parts + 15) / 16 * 16;
+  return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, 128), 2048);
+}
+
+#ifndef PA_Q8_LIST_ROUNDS
+#define PA_Q8_LIST_ROUNDS 3
+#endif
+inline bool q8_use_list(int64_t pairs, int32_t partitions, int32_t head_dim) {
+  return partitions >= 2 && pairs * partitions > (int64_t)PA_Q8_LIST_ROUNDS * q8_resident(head_dim);
+}
 
 // Tensor map of an 8-bit pool's codes: (byte of a 128-byte line, line of the
 // tile, kv head, K|V, block); box = the K and V tiles of one (block, head).
@@ -523,13 +824,28 @@ inline pa_status launch_decode_q8(const DecodeParams& p, cudaStream_t st) {
   CUtensorMap map;
   pa_status s = encode_q8_map(p.pool, p.num_kv_heads, D, p.num_blocks, &map);
   if (s != PA_OK) return s;
+  if (q8_by_warp((int64_t)p.num_seqs * p.num_kv_heads, p.max_seq_len)) {
+    auto warp_kernel = decode_q8_warp_kernel<T, D, NT, Code>;
+    static PerDevice<int32_t> smem_set;
+    cudaError_t e = set_smem_once(smem_set, warp_kernel, Q8Tile<D>::kSmem);
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode_q8: %s", cudaGetErrorString(e));
+    // no more stages than a sequence has blocks: short ones leave room for more CTAs
+    const int32_t stages = std::min<int32_t>(Q8Tile<D>::kStages, (p.max_seq_len + 15) / 16);
+    const int32_t ring = std::max<int32_t>(stages, 1) * Q8Tile<D>::kStage;
+    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads;
+    warp_kernel<<<(unsigned)((items + kQ8Warps - 1) / kQ8Warps), kQ8Warps * 32, kQ8Warps * ring + 1024, st>>>(
+        map, p, q8_layout(p.num_kv_heads, D), ring);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode_q8: launch failed: %s", cudaGetErrorString(e));
+    return PA_OK;
+  }
   auto kernel = decode_q8_kernel<T, D, NT, Code>;
   static PerDevice<int32_t> occupancy;  // resident CTAs per SM, with the shared-memory limit set once per device
   int32_t per_sm = 1;
   cudaError_t e = occupancy.get(&per_sm, [&](int32_t* v) {
     int32_t n = 0;
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8Smem);
-    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kQ8Warps * 32, kQ8Smem);
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Tile<D>::kSmem);
+    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kQ8Warps * 32, Q8Tile<D>::kSmem);
     *v = n > 0 ? n : 1;
     return r;
   });
@@ -539,7 +855,7 @@ inline pa_status launch_decode_q8(const DecodeParams& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kQ8Warps * 32);
-  cfg.dynamicSmemBytes = kQ8Smem;
+  cfg.dynamicSmemBytes = Q8Tile<D>::kSmem;
   cfg.stream = st;
   if (p.work_items == nullptr) {
     cfg.gridDim = dim3(p.max_partitions, p.num_kv_heads, p.num_seqs);
@@ -562,7 +878,8 @@ inline pa_status launch_decode_q8(const DecodeParams& p, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, kernel, map, p, q8_layout(p.num_kv_heads, D));
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode_q8: launch failed: %s", cudaGetErrorString(e));
   if (p.max_partitions <= 1) return PA_OK;
-  e = launch_partition_merge<T, D, true>(p, st);
+  // one CTA per head where its warps have partitions to share
+  e = p.max_partitions > 8 ? launch_decode_q8_merge<T, D, true>(p, st) : launch_decode_q8_merge<T, D, false>(p, st);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode_q8 (merge): launch failed: %s", cudaGetErrorString(e));
   return PA_OK;
 }

@@ -158,10 +158,10 @@ struct WorkspaceLayout {
   int32_t partitions;
 };
 
+// S: tokens of a partition.
 WorkspaceLayout workspace_layout(int32_t num_seqs, int32_t num_heads, const pa_pool_desc& pool,
-                                 int32_t max_seq_len) {
+                                 int32_t max_seq_len, int32_t S) {
   WorkspaceLayout w{0, 0, 0, 0, 0, 0};
-  const int32_t S = partition_tokens_for(num_seqs, pool, max_seq_len);
   w.partitions = (int32_t)(((int64_t)max_seq_len + S - 1) / S);
   if (w.partitions <= 1) return w;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -173,6 +173,11 @@ WorkspaceLayout workspace_layout(int32_t num_seqs, int32_t num_heads, const pa_p
   w.header_offset = up(w.items_offset + (size_t)num_seqs * w.partitions * sizeof(int32_t));
   w.total = w.header_offset + 2 * sizeof(int32_t);
   return w;
+}
+
+WorkspaceLayout workspace_layout(int32_t num_seqs, int32_t num_heads, const pa_pool_desc& pool,
+                                 int32_t max_seq_len) {
+  return workspace_layout(num_seqs, num_heads, pool, max_seq_len, partition_tokens_for(num_seqs, pool, max_seq_len));
 }
 
 template <typename T, int D>
@@ -551,7 +556,10 @@ pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool, c
 }
 
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads, pa_pool_desc pool, int32_t max_seq_len) {
-  return pa_decode_workspace_size(num_seqs, num_heads, pool, max_seq_len);
+  if (num_seqs <= 0 || num_heads <= 0 || max_seq_len <= 0 || pool.num_kv_heads <= 0 || pool.head_dim <= 0) return 0;
+  return workspace_layout(num_seqs, num_heads, pool, max_seq_len,
+                          pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, max_seq_len))
+      .total;
 }
 
 pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int32_t* block_tables,
@@ -567,13 +575,17 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int3
     return fail(PA_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 65535", fn, pool.num_kv_heads);
   if (num_seqs == 0) return PA_OK;
   const int32_t len = max_seq_len > 0 ? max_seq_len : 1;
-  const WorkspaceLayout w = workspace_layout(num_seqs, num_heads, pool, len);
+  const int32_t S = pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, len);
+  if (((int64_t)len + S - 1) / S > kMaxPartitions)
+    return fail(PA_ERR_UNSUPPORTED, "%s: max_seq_len %d needs more than %lld partitions of %d tokens", fn, max_seq_len,
+                (long long)kMaxPartitions, S);
+  const WorkspaceLayout w = workspace_layout(num_seqs, num_heads, pool, len, S);
   if (w.total > 0 && (!workspace || workspace_bytes < w.total))
     return fail(PA_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", fn, workspace_bytes, workspace, w.total);
   if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
   char* ws = reinterpret_cast<char*>(workspace);
-  const bool use_list = w.total && w.partitions >= kWorkListPartitions;
+  const bool use_list = pagedkv::q8_use_list((int64_t)num_seqs * pool.num_kv_heads, w.partitions, pool.head_dim);
   pagedkv::DecodeParams p = {};
   p.out = out;
   p.q = q;
@@ -591,7 +603,7 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int3
   p.group = num_heads / pool.num_kv_heads;
   p.num_blocks = pool.num_blocks;
   p.max_seq_len = max_seq_len;
-  p.partition_tokens = partition_tokens_for(num_seqs, pool, len);
+  p.partition_tokens = S;
   p.max_partitions = w.partitions > 0 ? w.partitions : 1;
   p.scale_log2 = scale * pagedkv::kLog2e;
   cudaStream_t st = (cudaStream_t)stream;
