@@ -415,7 +415,7 @@ pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,
  * inputs. All arrays are on the device. Nothing is allocated; the calls may be
  * captured in a CUDA graph. workspace: device, 4-byte aligned,
  * pa_tables_workspace_size(num_seqs) bytes, not used by another call at the
- * same time. num_seqs at most 2^20.
+ * same time. num_seqs at most 2^20, ring_size and num_slots at most 2^30.
  */
 size_t pa_tables_workspace_size(int32_t num_seqs);
 

@@ -668,6 +668,8 @@ pa_status check_tables(const char* fn, const void* tables, const void* lens, con
   if (num_seqs > kTablesMaxSeqs) return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs %d > %d", fn, num_seqs, kTablesMaxSeqs);
   if ((int64_t)max_blocks_per_seq * PA_BLOCK_SIZE > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: max_blocks %d * 16 tokens pass 32 bits", fn, max_blocks_per_seq);
+  if (ring_size > pagedkv::kTablesMost)
+    return fail(PA_ERR_UNSUPPORTED, "%s: ring_size %d > %d", fn, ring_size, pagedkv::kTablesMost);
   if (!ring || !state || !state_out || (num_seqs > 0 && (!tables || !lens || !asked || !lens_out)))
     return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
   if (!workspace || workspace_bytes < pagedkv::tables_workspace_bytes(num_seqs))
@@ -698,6 +700,8 @@ pa_status pa_tables_extend(int32_t* block_tables, int32_t max_blocks_per_seq, co
   if (s != PA_OK) return s;
   if (num_slots < 0 || row_tokens < 0)
     return fail(PA_ERR_INVALID_ARG, "%s: num_slots %d, row_tokens %d", fn, num_slots, row_tokens);
+  if (num_slots > pagedkv::kTablesMost)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_slots %d > %d", fn, num_slots, pagedkv::kTablesMost);
   if (row_tokens > 0 && (int64_t)num_seqs * row_tokens > num_slots)
     return fail(PA_ERR_INVALID_ARG, "%s: num_slots %d < num_seqs * row_tokens", fn, num_slots);
   if (!query_start || (num_slots > 0 && !slot_mapping)) return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);

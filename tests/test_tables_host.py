@@ -30,6 +30,7 @@ def test_extend_refuses_on_host():
                dict(sm=None), dict(so=None), dict(ws=C.c_void_p(18))):
         assert call(**kw) == 1, kw
     assert call(ns=(1 << 20) + 1) == 2 and call(mb=1 << 28) == 2
+    assert call(rs=(1 << 30) + 1) == 2 and call(n=(1 << 30) + 1) == 2
     assert call(ws=None) == 9 and call(wb=need - 1) == 9
 
 
