@@ -383,9 +383,9 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
 /*
  * pa_prefill over an 8-bit pool: the same operation, arguments, checks and
  * errors, with K_t and V_t = code * scale; q, out bf16. Products are formed on
- * the codes (exact in bf16) and accumulated in fp32; a probability times its
- * V scale is rounded to bf16 (2^-8 relative), as pa_prefill rounds its
- * probabilities. Supported: head_dim 128, num_heads / num_kv_heads in
+ * the codes (exact in bf16 and fp16) and accumulated in fp32; a probability
+ * times its V scale is rounded to fp16 (2^-11 relative). Where scores pass about
+ * 2^25 (off by units in fp32) a row may come out as 0. Supported: head_dim 128, num_heads / num_kv_heads in
  * {1, 2, 4, 8, 16}, scale >= 0 (else PA_ERR_INVALID_ARG).
  */
 pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,

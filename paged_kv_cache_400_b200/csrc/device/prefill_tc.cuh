@@ -57,17 +57,23 @@
 // one completion ahead of the last one its waiter consumed, so a parity wait
 // is never ambiguous.
 //
-// 8-bit pools (Code != void, see q8_common.cuh): K and V stages are the codes
-// as bf16, which holds every int8 and e4m3 code exactly, so the tensor-core
-// side is the same. The producers are four warps, one block slot of the tile
-// each, that read codes with plain 16-byte loads a tile ahead, convert them in
-// registers and store them where TMA would have put the rows; whatever codes
-// lie behind the sequence's end are finite and masked. The scales stay fp32: a
-// block's K scale k_b multiplies its 16 columns of S in the exponent's argument,
-// its V scale v_b enters there too,
-//     P = 2^(scale k_b s + log2 v_b - m) = v_b p,   l += (sum of the block's P) / v_b,
-// so both cost no instruction per element; m is the running maximum of the
-// whole argument. Zero V scales count as 1 over a zeroed tile.
+// 8-bit pools (Code != void, see q8_common.cuh): the K stages are the codes as
+// bf16, the V stages as fp16; both hold every int8 and e4m3 code exactly. The
+// producers are four warps, one block slot of the tile each, that read codes
+// with plain 16-byte loads a tile ahead, convert them in registers and store
+// them where TMA would have put the rows. The scales stay fp32: a block's K
+// scale k_b multiplies its 16 columns of S in the exponent's argument, its V
+// scale v_b enters there too,
+//     P = 2^(x + log2 v_b - m + 7) = 2^(7 - m) v_b 2^x,  x = scale log2 e k_b s,
+//     l += (sum of the block's P) / v_b,
+// so both cost no instruction per element; m is the running maximum of
+// x + log2 v_b, and P, at most 2^15, goes to fp16 (2^-11 relative, against 2^-8
+// of bf16; V's conversion from int8 takes 5 instructions per 4 codes instead of
+// 8, from e4m3 2 instead of 10: 512-token chunks behind 4096 tokens 356 -> 345
+// us with int8, 361 -> 341 us with e4m3). Zero V scales count as 1 over a
+// zeroed tile. m lies 2^-22 of itself above the maximum: huge scores, which fp32
+// spaces by more than a unit, then cannot push an exponent past fp16 (from
+// scores of about 2^25 on, where they are off by units, rows come out as 0).
 #pragma once
 
 #include <type_traits>
@@ -85,6 +91,7 @@ constexpr int kTcHalfBytes = kTcKeys * 128;       // 64 keys x 64 dims x bf16
 constexpr int kTcStageBytes = 4 * kTcHalfBytes;   // K lo, K hi, V lo, V hi
 constexpr int kTcQBytes = 128 * 256;              // one 128-row query tile x 128 dims x bf16
 constexpr float kTcRescaleLog2 = 8.0f;            // raise the reference max past this growth
+constexpr float kTcLift = 7.0f;                   // 8-bit pools: P is held 2^7 above its reference, at most 2^15 in fp16
 
 // Two query tiles of 128 rows share every staged KV tile: one CTA per SM (all
 // 512 tensor-memory columns, 225 KB of shared memory), a 4-deep KV ring.
@@ -481,9 +488,13 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
               return false;
             }
           }
-          if (v_b == 0.f) {
+          // V rows that must not count: under a zero scale, and behind the
+          // sequence's end (they may hold NaN codes, which P = 0 does not silence)
+          const int32_t live = v_b == 0.f ? 0 : u.L - (j * kTcBlocksPerTile + pw) * 16;
+          if (live < 16) {
 #pragma unroll
-            for (int i = 4; i < 8; ++i) c[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 4; i < 8; ++i)
+              if (4 * (i & 3) + row >= live) c[i] = make_uint4(0, 0, 0, 0);
           }
           uint8_t* st = kv_smem + s * kTcStageBytes;
 #pragma unroll
@@ -492,10 +503,14 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             uint8_t* line = st + tc_region(i >> 2, c16 >> 2) + key * 128;
             const int32_t ch = 2 * (c16 & 3);
             uint4 lo, hi;
-            q8_to_bf16(Code{}, c[i].x, lo.x, lo.y);
-            q8_to_bf16(Code{}, c[i].y, lo.z, lo.w);
-            q8_to_bf16(Code{}, c[i].z, hi.x, hi.y);
-            q8_to_bf16(Code{}, c[i].w, hi.z, hi.w);
+            auto convert = [&](uint32_t w, uint32_t& p0, uint32_t& p1) {
+              if (i < 4) q8_to_bf16(Code{}, w, p0, p1);
+              else q8_unpack(Code{}, w, false, p0, p1);
+            };
+            convert(c[i].x, lo.x, lo.y);
+            convert(c[i].y, lo.z, lo.w);
+            convert(c[i].z, hi.x, hi.y);
+            convert(c[i].w, hi.z, hi.w);
             *reinterpret_cast<uint4*>(line + ((ch ^ (key & 7)) << 4)) = lo;
             *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (key & 7)) << 4)) = hi;
           }
@@ -712,7 +727,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
     const int t = warp - Cfg::kMmaWarp;
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc_idesc_bf16(128, kTcKeys, false);
-      constexpr uint32_t idesc_pv = tc_idesc_bf16(128, 128, true);
+      constexpr uint32_t idesc_pv = kQ8 ? tc_idesc_f16(128, 128, true) : tc_idesc_bf16(128, 128, true);
       const uint32_t qa = smem_addr(q_smem) + t * kTcQBytes;
       const uint32_t kv_addr = smem_addr(kv_smem);
       const uint32_t tm = tmem + t * 256;
@@ -872,7 +887,9 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             m4[c >> 3] = max3(m4[c >> 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
           mt = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < kTcBlocksPerTile; ++b) mt = fmaxf(mt, fmaf(m4[b], bsc[b].x, bsc[b].y));
+          for (int b = 0; b < kTcBlocksPerTile; ++b)
+            mt = fmaxf(mt, fmaf(m4[b], bsc[b].x, bsc[b].y));
+          mt = fmaf(fabsf(mt), 0x1p-22f, mt);  // above what the exponents' roundings can add to the largest
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -923,7 +940,8 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
               }
               const float4 b = bsc[c / 8];
               scale2 = make_float2(b.x, b.x);
-              neg_m2 = make_float2(b.y - m_ref, b.y - m_ref);
+              const float c0 = b.y + kTcLift - m_ref;
+              neg_m2 = make_float2(c0, c0);
               rv = b.z;
             }
           }
@@ -936,7 +954,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             p1 = key0 + 2 * c + 1 <= P ? p1 : 0.f;
           }
           sum2[c & 1] = add2(sum2[c & 1], make_float2(p0, p1));
-          pw[c] = pack_bf16x2(p0, p1);
+          pw[c] = kQ8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         }
         if constexpr (kQ8) l = fmaf((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y), rv, l);
         else l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
@@ -960,7 +978,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
           // tile (its rows after the new tokens belong to the next sequence)
           // by plain stores, each warp its own valid rows. The warps of the
           // group meet on mbarriers, so that every wait is bounded.
-          const float inv = 1.f / l;
+          const float inv = kQ8 && !(l > 0.f) ? (l == 0.f ? 0.f : l) : 1.f / l;
           const bool whole = te == tb + QT;
           const int32_t row0 = (warp & 3) * 32;
           uint4* out4 = reinterpret_cast<uint4*>(p.out);

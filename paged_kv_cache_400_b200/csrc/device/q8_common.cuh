@@ -91,4 +91,26 @@ struct CodeE4m3 {
   }
 };
 
+// Four codes of one word -> two fp16 pairs: (b0, b1), (b2, b3) of the bytes.
+__device__ __forceinline__ void q8_unpack(CodeInt8, uint32_t w, bool interleaved, uint32_t& p, uint32_t& q) {
+  const uint32_t u = w ^ 0x80808080u;  // code + 128
+  const uint32_t a = __byte_perm(u, 0x64646464u, interleaved ? 0x4240 : 0x4140);
+  const uint32_t b = __byte_perm(u, 0x64646464u, interleaved ? 0x4341 : 0x4342);
+  const uint32_t bias = 0x64806480u;   // 1024 + 128
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p) : "r"(a), "r"(bias));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(q) : "r"(b), "r"(bias));
+}
+__device__ __forceinline__ void q8_unpack(CodeE4m3, uint32_t w, bool interleaved, uint32_t& p, uint32_t& q) {
+  if (interleaved) w = __byte_perm(w, 0, 0x3120);  // (b0, b2), (b1, b3)
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(p), "=r"(q)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
 }  // namespace pagedkv

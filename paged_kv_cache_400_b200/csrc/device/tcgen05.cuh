@@ -74,6 +74,11 @@ __host__ __device__ constexpr uint32_t tc_idesc_bf16(uint32_t M, uint32_t N, boo
          | ((M >> 4) << 24);
 }
 
+// The same with fp16 A and B (format 0).
+__host__ __device__ constexpr uint32_t tc_idesc_f16(uint32_t M, uint32_t N, bool b_mn_major) {
+  return tc_idesc_bf16(M, N, b_mn_major) & ~((7u << 7) | (7u << 10));
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets (all in 16-byte units in the descriptor).
 __device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
