@@ -349,14 +349,12 @@ int64_t pa_pool_block_bytes(pa_pool_desc pool);
  * tile whose scale is 0), and either sets PA_DEVERR_NONFINITE.
  * k, v: device, [num_tokens][num_kv_heads][head_dim] contiguous, io_dtype,
  *       16-byte aligned.
- * slot_mapping: as pa_reshape_and_cache. All tokens of one block must lie
- *       within 32 consecutive entries (padding may lie between them), as a
- *       sequence's tokens in order do; one that follows later than that, but
- *       within 31 entries of the block's previous one, is not written and sets
- *       PA_DEVERR_SLOT. A block that comes back after a longer gap would be
- *       written by two warps at once: the caller must not do that (within 62
- *       entries it sets PA_DEVERR_SLOT). Two tokens with the same slot (within
- *       those 32 entries): the later one is stored.
+ * slot_mapping: as pa_reshape_and_cache. A block's tokens, each within 31
+ *       entries of the block's one before (padding may lie between, and order
+ *       does not matter), are written together; of two with the same slot the
+ *       later one is stored. A block may come back after a longer gap only with
+ *       the rows and values it had before, as when requests that share a prefix
+ *       are admitted in one step: it is then written twice at the same time.
  */
 pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool,
                                   const int64_t* slot_mapping, int32_t num_tokens,

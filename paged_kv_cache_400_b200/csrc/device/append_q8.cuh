@@ -8,9 +8,13 @@
 //
 // One warp owns a tile, so a scale and the rows under it change together and
 // nothing is summed or ordered across warps: the warp of a block's first token
-// in slot_mapping (its leader) gathers the block's other tokens from the 31
-// entries behind it; the other tokens lead nothing. A row named twice takes the
-// later token.
+// in slot_mapping (its leader: none of the 31 entries before it names the block)
+// gathers the block's other tokens behind it, as long as each lies within 31
+// entries of the one before; these lead nothing. A row named twice takes the
+// later token. A block that comes back after a longer gap has a second leader,
+// which writes at the same time: requests that share a prefix and are admitted
+// in one step name its blocks with the same rows and values, so both store the
+// same bytes.
 //
 // Bound by its bytes (reads T * Hkv * D elements twice over for K and V, writes
 // half or a quarter as many) for many tokens, by latency for few. A warp looks
@@ -62,7 +66,7 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     uint32_t w[4];
     __device__ __forceinline__ float get(int c) const { return Bits<T>::get(w, c); }
   };
-  __shared__ uint8_t row_src[kAppendQ8Warps][16];
+  __shared__ int32_t row_src[kAppendQ8Warps][16];
   const int32_t warp = threadIdx.x >> 5;
   const int32_t lane = threadIdx.x & 31;
   const int32_t h = blockIdx.y;
@@ -76,7 +80,7 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
   const int64_t raw0 = slot_of((int64_t)t0 + lane), raw_prev = slot_of((int64_t)t0 - 32 + lane);
   const int64_t raw1 = slot_of((int64_t)t0 + 32 + lane), raw2 = slot_of((int64_t)t0 + 64 + lane);
   auto block_of = [&](int64_t s) -> int32_t { return s >= 0 && s < num_slots ? (int32_t)(s >> 4) : -1; };
-  const int32_t b0 = block_of(raw0), b_prev = block_of(raw_prev), b1 = block_of(raw1), b2 = block_of(raw2);
+  const int32_t b0 = block_of(raw0), b_prev = block_of(raw_prev);
   if (reports && lane < run && raw0 >= num_slots) raise_device_error(PA_DEVERR_SLOT);
 
   // leaders: the run's first entry of a block that none of the 31 entries before it names
@@ -89,40 +93,37 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     todo &= todo - 1;
     const int32_t blk = __shfl_sync(kAll, b0, first);
     if (__any_sync(kAll, b_prev == blk && lane > first)) continue;  // an earlier entry leads
-    // its entries: first .. first + 31; tokens of the block behind them are not written
-    const uint32_t in0 = __ballot_sync(kAll, b0 == blk), in1 = __ballot_sync(kAll, b1 == blk && lane < first);
-    if (__any_sync(kAll, (b1 == blk && lane >= first) || (b2 == blk && lane + 1 < first)) && reports && lane == 0)
-      raise_device_error(PA_DEVERR_SLOT);
-
     uint8_t* tile = pool + (size_t)blk * lay.block_bytes + ((size_t)kv * num_kv_heads + h) * 16 * D;
     float* scale_at = reinterpret_cast<float*>(pool + q8_scale_at(lay, blk, kv, h, num_kv_heads));
     const float s_old = *scale_at;
 
-    // row -> entry, counted from t0 (0xff: not written now); of a row's entries the latest
+    // row -> its latest entry, counted from t0 (-1: not written now), 32 entries at a time
     __syncwarp();
-    if (lane < 16) row_src[warp][lane] = 0xff;
+    if (lane < 16) row_src[warp][lane] = -1;
     __syncwarp();
-    {
-      const bool m0 = (in0 >> lane) & 1u, m1 = (in1 >> lane) & 1u;
-      const int32_t r0 = m0 ? (int32_t)(raw0 & 15) : 32 + lane, r1 = m1 ? (int32_t)(raw1 & 15) : 32 + lane;
-      const uint32_t eq0 = __match_any_sync(kAll, r0);
-      if (m0 && (eq0 >> lane) == 1u) row_src[warp][r0] = (uint8_t)lane;
+    int64_t raw = raw0;
+    uint32_t in = __ballot_sync(kAll, b0 == blk);
+    for (int32_t w = 0;;) {
+      const bool member = (in >> lane) & 1u;
+      const int32_t r = member ? (int32_t)(raw & 15) : 32 + lane;
+      const uint32_t same = __match_any_sync(kAll, r);
+      if (member && (same >> lane) == 1u) row_src[warp][r] = 32 * w + lane;
       __syncwarp();
-      if (in1) {
-        const uint32_t eq1 = __match_any_sync(kAll, r1);
-        if (m1 && (eq1 >> lane) == 1u) row_src[warp][r1] = (uint8_t)(32 + lane);
-        __syncwarp();
-      }
+      const int32_t last = 31 - __clz(in);  // of this window
+      ++w;
+      raw = w == 1 ? raw1 : w == 2 ? raw2 : slot_of((int64_t)t0 + 32 * w + lane);
+      in = __ballot_sync(kAll, block_of(raw) == blk);
+      if (in == 0 || __ffs(in) + 31 - last > 31) break;
     }
-    const bool fresh = row_src[warp][0] != 0xff;
+    const bool fresh = row_src[warp][0] >= 0;
 
     Words x[kSteps];
     uint32_t written = 0;  // bit i: this lane's row of step i is new
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const uint32_t e = row_src[warp][i * kRows + my_row];
+      const int32_t e = row_src[warp][i * kRows + my_row];
       x[i].q = make_uint4(0, 0, 0, 0);
-      if (e != 0xffu) {
+      if (e >= 0) {
         written |= 1u << i;
         x[i].q = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(t0 + e) * num_kv_heads + h) * D + my_col));
       }

@@ -5,7 +5,7 @@ which are admitted (their prompt K/V are (re)written: recompute), which grow a
 block, which are preempted or finish; then, for every layer, the step's device
 work runs through the C ABI: copy-on-write block copies, the prompt-token
 append, then the decode-token append and paged decode over the running batch
-in one call (pa_append_decode)
+in one call (pa_append_decode; over 8-bit pools, kv_code, in two)
 ("vLLM 原理：PagedAttention 和 Continuous Batching" / "vLLM 的调度 / 调度流程";
 "大模型推理性能优化：PagedAttention与Continuous Batching原理与实践" §2.3).
 
@@ -59,12 +59,16 @@ class StepIndices:
 class DecodeEngine:
     def __init__(self, num_blocks, num_layers, num_heads, num_kv_heads, head_dim, arrival_step,
                  prompt_len, output_len, table_width, scale, device, dtype=torch.bfloat16,
-                 max_seq_len=None, prompt_tokens=None, swap_host_blocks=0):
+                 max_seq_len=None, prompt_tokens=None, swap_host_blocks=0, kv_code=None):
         """prompt_tokens: per-request prompt token ids to turn on automatic
         prefix caching (admission reuses cached prompt blocks and only the KV
         after the cached prefix is written). swap_host_blocks: pinned host
-        blocks per layer for swap-mode preemption (0: recompute only)."""
+        blocks per layer for swap-mode preemption (0: recompute only).
+        kv_code: "int8" or "e4m3" for 8-bit pools (binding.Q8Pool); dtype is
+        then that of queries, new K/V and outputs."""
         self.device = torch.device(device)
+        self.dtype = dtype
+        self.kv_code = kv_code
         self.num_layers = num_layers
         self.num_heads = num_heads
         self.num_kv_heads = num_kv_heads
@@ -81,11 +85,19 @@ class DecodeEngine:
         self.host_pools = []
         if swap_host_blocks > 0:
             self.sched.set_swap(swap_host_blocks)
-        shape = (num_blocks, 2, num_kv_heads, bd.BLOCK_SIZE, head_dim)
-        self.pools = [torch.empty(shape, dtype=dtype, device=self.device) for _ in range(num_layers)]
-        if swap_host_blocks > 0:
-            hshape = (swap_host_blocks,) + shape[1:]
-            self.host_pools = [torch.empty(hshape, dtype=dtype, pin_memory=True) for _ in range(num_layers)]
+        if kv_code is not None:
+            self.pools = [bd.Q8Pool(num_blocks, num_kv_heads, head_dim, kv_code, self.device)
+                          for _ in range(num_layers)]
+            if swap_host_blocks > 0:
+                hshape = (swap_host_blocks, bd.Q8Pool.block_bytes(num_kv_heads, head_dim, kv_code))
+                self.host_pools = [bd.Q8Pool.wrap(torch.empty(hshape, dtype=torch.uint8, pin_memory=True),
+                                                  num_kv_heads, head_dim, kv_code) for _ in range(num_layers)]
+        else:
+            shape = (num_blocks, 2, num_kv_heads, bd.BLOCK_SIZE, head_dim)
+            self.pools = [torch.empty(shape, dtype=dtype, device=self.device) for _ in range(num_layers)]
+            if swap_host_blocks > 0:
+                hshape = (swap_host_blocks,) + shape[1:]
+                self.host_pools = [torch.empty(hshape, dtype=dtype, pin_memory=True) for _ in range(num_layers)]
         self._ws = None
         self._ws_bytes = 0
         self.prefill_out = None
@@ -157,6 +169,21 @@ class DecodeEngine:
         return bt, sl, torch.from_numpy(qs).to(dev), int(counts.max()) if len(counts) else 0
 
     # ---- device side -------------------------------------------------------------
+    # the three calls of a layer on the engine's kind of pool
+    def append(self, k, v, pool, slots):
+        (bd.pa_reshape_and_cache_q8 if self.kv_code else bd.pa_reshape_and_cache)(k, v, pool, slots)
+
+    def prefill(self, out, q, pool, tables, lens, query_start, max_query_len):
+        (bd.pa_prefill_q8 if self.kv_code else bd.pa_prefill)(out, q, pool, tables, lens, query_start, self.scale,
+                                                              max_query_len)
+
+    def append_decode(self, out, q, k, v, pool, slots, tables, lens, ws):
+        if self.kv_code:
+            bd.pa_reshape_and_cache_q8(k, v, pool, slots)
+            bd.pa_decode_q8(out, q, pool, tables, lens, self.scale, self.max_seq_len, ws)
+        else:
+            bd.pa_append_decode(out, q, k, v, pool, slots, tables, lens, self.scale, self.max_seq_len, ws)
+
     def workspace(self, batch):
         """A workspace large enough for `batch` sequences (grown on demand: the
         partition size, hence the bytes needed, depends on the batch)."""
@@ -211,23 +238,22 @@ class DecodeEngine:
         pf = self.prefill_indices(idx) if (ps is not None and "q_prompt" in inputs[0]) else None
         self.prefill_out = [] if pf is not None else None
         outs = out if out is not None else [torch.empty(n, self.num_heads, self.head_dim,
-                                                         dtype=self.pools[0].dtype, device=dev)
+                                                         dtype=self.dtype, device=dev)
                                              for _ in range(self.num_layers)]
         for l, pool in enumerate(self.pools):
             x = inputs[l]
             if cs is not None:
                 bd.pa_copy_blocks(pool, cs, cd)
             if ps is not None:
-                bd.pa_reshape_and_cache(x["k_prompt"], x["v_prompt"], pool, ps)
+                self.append(x["k_prompt"], x["v_prompt"], pool, ps)
             if pf is not None:
                 # the admitted prompts' new positions attend causally over their KV
                 pbt, psl, pqs, pmax = pf
                 po = torch.empty_like(x["q_prompt"])
-                bd.pa_prefill(po, x["q_prompt"], pool, pbt, psl, pqs, self.scale, pmax)
+                self.prefill(po, x["q_prompt"], pool, pbt, psl, pqs, pmax)
                 self.prefill_out.append(po)
             # each running request's new token appended and attended in one call
-            bd.pa_append_decode(outs[l], x["q"], x["k_dec"], x["v_dec"], pool, ds, bt, sl, self.scale,
-                                self.max_seq_len, ws)
+            self.append_decode(outs[l], x["q"], x["k_dec"], x["v_dec"], pool, ds, bt, sl, ws)
         return outs
 
 
@@ -251,7 +277,7 @@ class GraphedLayers:
         self.max_batch = ((max_batch + bucket - 1) // bucket) * bucket
         dev, L = engine.device, engine.num_layers
         H, Hkv, D, W = engine.num_heads, engine.num_kv_heads, engine.head_dim, engine.table_width
-        dt = engine.pools[0].dtype
+        dt = engine.dtype
         B = self.max_batch
         self.q = torch.zeros(L, B, H, D, dtype=dt, device=dev)
         self.k = torch.zeros(L, B, Hkv, D, dtype=dt, device=dev)
@@ -268,8 +294,8 @@ class GraphedLayers:
     def _calls(self, n):
         e = self.eng
         for l, pool in enumerate(e.pools):
-            bd.pa_append_decode(self.out[l, :n], self.q[l, :n], self.k[l, :n], self.v[l, :n], pool,
-                                self.slots[:n], self.bt[:n], self.sl[:n], e.scale, e.max_seq_len, self.ws)
+            e.append_decode(self.out[l, :n], self.q[l, :n], self.k[l, :n], self.v[l, :n], pool,
+                            self.slots[:n], self.bt[:n], self.sl[:n], self.ws)
 
     def _graph(self, n):
         g = self.graphs.get(n)
@@ -310,10 +336,10 @@ class GraphedLayers:
             if cs is not None:
                 bd.pa_copy_blocks(pool, cs, cd)
             if ps is not None:
-                bd.pa_reshape_and_cache(inputs[l]["k_prompt"], inputs[l]["v_prompt"], pool, ps)
+                e.append(inputs[l]["k_prompt"], inputs[l]["v_prompt"], pool, ps)
             if pf is not None:
                 po = torch.empty_like(inputs[l]["q_prompt"])
-                bd.pa_prefill(po, inputs[l]["q_prompt"], pool, pf[0], pf[1], pf[2], e.scale, pf[3])
+                e.prefill(po, inputs[l]["q_prompt"], pool, pf[0], pf[1], pf[2], pf[3])
                 e.prefill_out.append(po)
         # static buffers: this step's rows, then inert padding up to the bucket
         self.bt[:n].copy_(torch.from_numpy(idx.block_tables), non_blocking=True)

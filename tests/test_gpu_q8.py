@@ -132,14 +132,27 @@ def test_append_bad_slots():
     pk.pa_reshape_and_cache_q8(k.to(DEV), k.to(DEV), p, torch.tensor([16, 64, 17, 1 << 40], device=DEV))
     assert pk.pa_get_device_error() == pk.PA_DEVERR_SLOT
     assert np.array_equal(host(p)[0], codes) and np.array_equal(host(p)[1], scales)
-    # a block's token behind its 32-entry window is not written
-    slots = [0] + [-1] * 19 + [1] + [-1] * 19 + [2] + [-1] * 3
-    codes, scales = host(p)
-    k = rows(len(slots), 2, 64, "f32", 2)
-    oq.append(codes, scales, k.numpy(), k.numpy(), slots[:32], "int8")
-    pk.pa_reshape_and_cache_q8(k.to(DEV), k.to(DEV), p, torch.tensor(slots, device=DEV))
-    assert pk.pa_get_device_error() == pk.PA_DEVERR_SLOT
-    assert np.array_equal(host(p)[0], codes) and np.array_equal(host(p)[1], scales)
+
+@CODE
+@pytest.mark.parametrize("lead", [0, 1, 14, 15, 16, 37])
+def test_append_tokens_far_apart(lead, code):
+    """A block's tokens over several windows of 32 entries, each within 31 of the one before; rows
+    named again; a neighbour block in between."""
+    p = make_pool(6, 2, 64, code, seed=4)
+    slots = [-1] * lead + [16 + 3] + [-1] * 30 + [16 + 9] + [32 + i for i in range(16)] + [16 + 3] + [-1] * 30 \
+        + [16 + 4, 16 + 0] + [-1] * 25 + [16 + 9] + [-1] * 40
+    check_append(p, rows(len(slots), 2, 64, "f32", 2), rows(len(slots), 2, 64, "f32", 3), slots)
+
+
+@CODE
+@pytest.mark.parametrize("gap", [0, 7, 15, 16, 31, 60, 200])
+def test_append_shared_prefix_in_one_call(gap, code):
+    """Two requests of a step write the same blocks with the same values, at any distance."""
+    p = make_pool(40, 2, 128, code, seed=5)
+    k, v = rows(32 + gap + 40, 2, 128, "bf16", 6), rows(32 + gap + 40, 2, 128, "bf16", 7)
+    k[32 + gap:64 + gap], v[32 + gap:64 + gap] = k[:32], v[:32]
+    slots = list(range(32)) + list(range(100, 100 + gap)) + list(range(32)) + list(range(400, 408))
+    check_append(p, k, v, slots)
 
 
 @CODE
