@@ -401,9 +401,8 @@ pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,
  * block ids, ring_state int32 {head, count, ...}: entries head .. head + count
  * - 1 (modulo ring_size) are free, the head first ([C] §2.2 keeps the free
  * blocks in a deque). A ring_size of num_blocks holds any state. The calls
- * write int32 [4] {head, count, moved, refused}: `moved` the tokens granted
- * (extend) or blocks given back (release), `refused` the requests that asked
- * and got nothing. Blocks are taken and given back in request and table order,
+ * write int32 [4] {head, count, tokens, refused}: `tokens` the tokens granted
+ * (0 by release), `refused` the requests that asked and got nothing. Blocks are taken and given back in request and table order,
  * as pa_bm_allocate, pa_bm_append_slot and pa_bm_free do for one sequence after
  * another, so tables and slots are the host block manager's. The requests own
  * their blocks alone: the calls know no shared blocks (fork and copy-on-write

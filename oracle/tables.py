@@ -84,4 +84,4 @@ def release(tables, lens, finished, ring, head, count, num_blocks):
             if not 0 <= tables[b][e] < num_blocks:
                 errors |= 2
             back += 1
-    return out, [state[0], state[1] + back, back, refused], errors
+    return out, [state[0], state[1] + back, 0, refused], errors

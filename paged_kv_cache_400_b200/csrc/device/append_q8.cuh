@@ -39,6 +39,13 @@ template <> struct Bits<float> {
   __device__ __forceinline__ static uint32_t max_abs(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
   __device__ __forceinline__ static uint32_t widest(uint32_t m) { return m; }
   __device__ __forceinline__ static float get(const uint32_t* w, int c) { return __uint_as_float(w[c]); }
+  // the pattern of a, or of the largest finite value below it
+  __device__ __forceinline__ static uint32_t finite(float a) { return min(__float_as_uint(a), 0x7f7fffffu); }
+  // NaN -> 0, an infinity -> `most` with its sign
+  __device__ __forceinline__ static uint32_t replace_odd(uint32_t w, uint32_t most) {
+    const uint32_t a = w & 0x7fffffffu;
+    return a < 0x7f800000u ? w : a > 0x7f800000u ? 0u : (w & 0x80000000u) | most;
+  }
 };
 template <> struct Bits<__nv_bfloat16> {
   __device__ __forceinline__ static uint32_t max_abs(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
@@ -46,12 +53,25 @@ template <> struct Bits<__nv_bfloat16> {
   __device__ __forceinline__ static float get(const uint32_t* w, int c) {
     return __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
   }
+  // to nearest: 2^-9 off at most, which the codes' own rounding takes up
+  __device__ __forceinline__ static uint32_t finite(float a) {
+    return min((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)), 0x7f7fu);
+  }
+  __device__ __forceinline__ static uint32_t replace_odd(uint32_t w, uint32_t most) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const uint32_t x = (w >> h) & 0xffffu, a = x & 0x7fffu;
+      out |= (a < 0x7f80u ? x : a > 0x7f80u ? 0u : (x & 0x8000u) | most) << h;
+    }
+    return out;
+  }
 };
 
 // Warp (4 x + w, head y, kv z) serves the leaders among entries
 // [run * (4 x + w), + run).
 template <typename T, int D, typename Code>
-__global__ void __launch_bounds__(kAppendQ8Warps * 32)
+__global__ void __launch_bounds__(kAppendQ8Warps * 32, 6)
 append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ pool,
                  const int64_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
                  Q8Layout lay, int32_t run) {
@@ -60,6 +80,7 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
   constexpr int kLanes = D / E;         // lanes of a row
   constexpr int kRows = 32 / kLanes;    // rows of a step
   constexpr int kSteps = 16 / kRows;
+  constexpr int C = kSteps < 8 ? kSteps : 8;  // steps held in registers (of 16, fp32 rows of 128, half at a time)
   using Codes = Vec<uint8_t, E>;
   union Words {  // 16 bytes of a row
     uint4 q;
@@ -117,34 +138,45 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     }
     const bool fresh = row_src[warp][0] >= 0;
 
-    Words x[kSteps];
+    // rows of steps c0 .. c0 + C - 1
+    Words x[C];
     uint32_t written = 0;  // bit i: this lane's row of step i is new
+    auto load = [&](int c0) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int32_t e = row_src[warp][i * kRows + my_row];
-      x[i].q = make_uint4(0, 0, 0, 0);
-      if (e >= 0) {
-        written |= 1u << i;
-        x[i].q = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(t0 + e) * num_kv_heads + h) * D + my_col));
+      for (int i = 0; i < C; ++i) {
+        const int32_t e = row_src[warp][(c0 + i) * kRows + my_row];
+        x[i].q = make_uint4(0, 0, 0, 0);
+        if (e >= 0) {
+          written |= 1u << (c0 + i);
+          x[i].q = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(t0 + e) * num_kv_heads + h) * D + my_col));
+        }
       }
-    }
+    };
     // largest magnitude, on the bit patterns
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int c0 = 0; c0 < kSteps; c0 += C) {
+      load(c0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) top = Bits<T>::max_abs(top, x[i].w[c]);
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top = Bits<T>::max_abs(top, x[i].w[c]);
+    }
     top = __reduce_max_sync(kAll, Bits<T>::widest(top));
     const bool odd = top >= 0x7f800000u;  // a NaN or an infinity among the rows
     if (odd) {
       top = 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kSteps; c0 += C) {
+        load(c0);
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int c = 0; c < E; ++c) {
-          const uint32_t a = __float_as_uint(fabsf(x[i].get(c)));
-          if (a < 0x7f800000u) top = max(top, a);
-        }
+          for (int c = 0; c < E; ++c) {
+            const uint32_t a = __float_as_uint(fabsf(x[i].get(c)));
+            if (a < 0x7f800000u) top = max(top, a);
+          }
+      }
       top = __reduce_max_sync(kAll, top);
       if (lane == 0) raise_device_error(PA_DEVERR_NONFINITE);
     }
@@ -156,43 +188,52 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     if (!fresh && s_new > s_old) {
       // rows that stay: coded again at the grown scale
       const float ratio = __fdiv_rn(s_old, s_new);
-      Codes c[kSteps];
+#pragma unroll 1
+      for (int c0 = 0; c0 < kSteps; c0 += 4) {
+        Codes c[4];
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (!((written >> i) & 1u)) c[i] = *reinterpret_cast<const Codes*>(tile + (i * kRows + my_row) * D + my_col);
+        for (int i = 0; i < 4; ++i)
+          if (!((written >> (c0 + i)) & 1u))
+            c[i] = *reinterpret_cast<const Codes*>(tile + ((c0 + i) * kRows + my_row) * D + my_col);
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        if ((written >> i) & 1u) continue;
+        for (int i = 0; i < 4; ++i) {
+          if ((written >> (c0 + i)) & 1u) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e) c[i].v[e] = (uint8_t)Code::encode(__fmul_rn(Code::decode(c[i].v[e]), ratio));
-        *reinterpret_cast<Codes*>(tile + (i * kRows + my_row) * D + my_col) = c[i];
+          for (int e = 0; e < E; ++e) c[i].v[e] = (uint8_t)Code::encode(__fmul_rn(Code::decode(c[i].v[e]), ratio));
+          *reinterpret_cast<Codes*>(tile + ((c0 + i) * kRows + my_row) * D + my_col) = c[i];
+        }
       }
     }
-    // the values are unpacked again here: kept since the maximum they would
-    // take twice the registers of the rows
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int c0 = 0; c0 < kSteps; c0 += C) {
+      if (kSteps > C) {
+        load(c0);  // a second time, from L1
+      } else {
+        // the values are unpacked again: kept since the maximum they would take
+        // twice the registers of the rows
 #pragma unroll
-      for (int c = 0; c < 4; ++c) asm volatile("" : "+r"(x[i].w[c]));
+        for (int i = 0; i < C; ++i)
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (!((written >> i) & 1u)) continue;
-      Vec<uint32_t, E / 4> c;
-      if (!odd) {
+          for (int c = 0; c < 4; ++c) asm volatile("" : "+r"(x[i].w[c]));
+      }
+      if (odd) {
+        // NaN -> 0, an infinity -> what the largest code of its sign stands for
+        const uint32_t most = Bits<T>::finite(__fmul_rn(Code::kMax, s_new));
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[i].w[c] = Bits<T>::replace_odd(x[i].w[c], most);
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        if (!((written >> (c0 + i)) & 1u)) continue;
+        Vec<uint32_t, E / 4> c;
 #pragma unroll
         for (int e = 0; e < E; e += 4)
           c.v[e / 4] = Code::encode4(__fmul_rn(x[i].get(e), inv), __fmul_rn(x[i].get(e + 1), inv),
                                      __fmul_rn(x[i].get(e + 2), inv), __fmul_rn(x[i].get(e + 3), inv));
-      } else {
-        for (int e = 0; e < E / 4; ++e) c.v[e] = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float y = x[i].get(e);
-          if (!(fabsf(y) <= FLT_MAX)) y = y != y ? 0.f : copysignf(FLT_MAX, y);  // NaN -> 0, inf -> the largest code
-          c.v[e / 4] |= Code::encode(__fmul_rn(y, inv)) << (8 * (e % 4));
-        }
+        *reinterpret_cast<Vec<uint32_t, E / 4>*>(tile + ((c0 + i) * kRows + my_row) * D + my_col) = c;
       }
-      *reinterpret_cast<Vec<uint32_t, E / 4>*>(tile + (i * kRows + my_row) * D + my_col) = c;
     }
     if (lane == 0 && (fresh || s_new != s_old)) *scale_at = s_new;
   }

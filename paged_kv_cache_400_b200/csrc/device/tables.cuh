@@ -47,7 +47,7 @@ struct TablesParams {
   int32_t* lens_out;        // [B]
   int32_t* query_start;     // [B + 1] (extend)
   int64_t* slots;           // [num_slots] (extend)
-  int32_t* state_out;       // head, count, tokens | blocks, refused requests
+  int32_t* state_out;       // head, count, tokens granted, refused requests
   int32_t* ws_starts;       // [B + 1] workspace: first position of each request
   int32_t* ws_old;          // [B] workspace: old length
   int32_t* ws_first;        // [B] workspace: first of the request's ring entries, from the head
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, 
       if (kExtend && (h += moved) >= t.ring_size) h -= t.ring_size;
       t.state_out[0] = usable ? h : head_in;
       t.state_out[1] = !usable ? count_in : kExtend ? count - moved : count + moved;
-      t.state_out[2] = (int32_t)granted0;
+      t.state_out[2] = kExtend ? (int32_t)granted0 : 0;
       t.state_out[3] = refused;
     }
   }
