@@ -137,14 +137,24 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// Lane i's table entry of partition `part`: the id of block rank + i * W, where
+// the table has such an entry. It does not depend on the sequence's length, so
+// the two can be asked for together.
+__device__ __forceinline__ int32_t q8_table_entry(const DecodeParams& p, int32_t part, int32_t b, int32_t rank,
+                                                  int32_t W) {
+  const int64_t e = (int64_t)part * (p.partition_tokens >> 4) + rank + (int64_t)(threadIdx.x & 31) * W;
+  return e < p.max_blocks ? __ldg(p.block_tables + (size_t)b * p.max_blocks + e) : -1;
+}
+
 // Attention over partition `part` of sequence b for KV head g (all G query
 // heads, NT = ceil(G / 8) tiles of 8), by W warps: a CTA (4), or one warp on its
-// own (then part 0, the whole sequence). `phase` as in decode_partition.
+// own (then part 0, the whole sequence). entry: q8_table_entry's; `phase` as in
+// decode_partition.
 template <typename T, int D, int NT, typename Code, int W>
 __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, const DecodeParams& p,
                                                     const Q8Layout& lay, uint8_t* smem, int32_t ring_bytes,
                                                     Q8Shared& sh, int32_t part, int32_t g, int32_t b, int32_t L,
-                                                    uint32_t& phase) {
+                                                    int32_t entry, uint32_t& phase) {
   using Tile = Q8Tile<D>;
   constexpr int S = Tile::kStages;
   constexpr int KK = D / 16;                              // k-steps of QK, row tiles of PV
@@ -173,11 +183,25 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   const int32_t my = nb > rank ? (nb - rank + W - 1) / W : 0;
   uint8_t* wsm = smem + warp * ring_bytes;
   const uint32_t wsm_addr = smem_addr(wsm);
-  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks + (t0 >> 4);
+
+  // the queries' words, in flight while the block ids and the first blocks arrive
+  using QWord = Vec<T, 4>;
+  QWord qw[NT][KK];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      const int32_t head = 8 * nt + gid;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qw[nt][kk].v[i] = Elem<T>::from_f32(0.f);
+      if (head < G)
+        qw[nt][kk] = *reinterpret_cast<const QWord*>(reinterpret_cast<const T*>(p.q) +
+                                                     ((size_t)b * H + (size_t)g * G + head) * D + 16 * kk + 4 * tig);
+    }
 
   // lane i holds the id of the warp's i-th block and, once they arrive, its
   // scales: k_b, log2 v_b and 1 / v_b
-  const int32_t my_blk = lane < my ? __ldg(table + rank + lane * W) : -1;
+  const int32_t my_blk = lane < my ? entry : -1;
   const bool my_ok = my_blk >= 0 && my_blk < p.num_blocks;
   if (lane < my && !my_ok) raise_device_error(PA_DEVERR_BLOCK);
   const uint32_t ok_mask = __ballot_sync(0xffffffffu, my_ok);
@@ -220,20 +244,15 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   float qsum[NT][2];  // 128 / unit * the sum of the scaled query (kBias)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int32_t head = 8 * nt + gid;
     float x[KK][4];
     float a = 0.f;
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      if (head < G) {
-        load_f32<T, 4>(reinterpret_cast<const T*>(p.q) + ((size_t)b * H + (size_t)g * G + head) * D + 16 * kk + 4 * tig,
-                       x[kk]);
-      } else {
-        x[kk][0] = x[kk][1] = x[kk][2] = x[kk][3] = 0.f;
-      }
+    for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a = fmaxf(a, fabsf(x[kk][i]));
-    }
+      for (int i = 0; i < 4; ++i) {
+        x[kk][i] = Elem<T>::to_f32(qw[nt][kk].v[i]);
+        a = fmaxf(a, fabsf(x[kk][i]));
+      }
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
     // exponent of a, kept where both powers of two below are normal
@@ -562,9 +581,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
   const int32_t warp = threadIdx.x >> 5;
   const int32_t lane = threadIdx.x & 31;
   grid_dependents_launch();
-  int32_t grid_len = 0;
+  int32_t grid_len = 0, entry = -1;
   if (p.work_items == nullptr) {
     const int32_t part = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+    entry = q8_table_entry(p, part, b, warp, kQ8Warps);
     grid_len = checked_len(p, b, part == 0 && g == 0 && threadIdx.x == 0);
     if (grid_len == 0) {
       if (part == 0) {
@@ -586,7 +606,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
   uint32_t phase = 0;
   if (p.work_items == nullptr) {
     decode_q8_partition<T, D, NT, Code, kQ8Warps>(tmap, p, lay, smem, Q8Tile<D>::kRing, sh, blockIdx.x, blockIdx.y,
-                                                  blockIdx.z, grid_len, phase);
+                                                  blockIdx.z, grid_len, entry, phase);
     return;
   }
   grid_dependency_wait();  // the plan kernel's item list is complete
@@ -602,9 +622,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, Q8Lay
     if (threadIdx.x == 0) next = atomicAdd(p.work_header + 1, 1);  // in flight during the item
     const uint32_t bp = (uint32_t)__ldcg(p.work_items + item / p.num_kv_heads);
     const int32_t g = item % p.num_kv_heads;
-    const int32_t b = (int32_t)(bp >> 16);
-    decode_q8_partition<T, D, NT, Code, kQ8Warps>(tmap, p, lay, smem, Q8Tile<D>::kRing, sh, (int32_t)(bp & 0xffffu), g, b,
-                                                  checked_len(p, b, false), phase);
+    const int32_t b = (int32_t)(bp >> 16), part = (int32_t)(bp & 0xffffu);
+    entry = q8_table_entry(p, part, b, warp, kQ8Warps);
+    decode_q8_partition<T, D, NT, Code, kQ8Warps>(tmap, p, lay, smem, Q8Tile<D>::kRing, sh, part, g, b,
+                                                  checked_len(p, b, false), entry, phase);
     fence_proxy_async_smem();  // the item's shared-memory reads precede the next item's TMA writes
     if (threadIdx.x == 0) sh.next_item = next;
     __syncthreads();
@@ -627,6 +648,7 @@ decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, 
   const int64_t item = (int64_t)blockIdx.x * kQ8Warps + warp;
   if (item >= (int64_t)p.num_seqs * p.num_kv_heads) return;
   const int32_t b = (int32_t)(item / p.num_kv_heads), g = (int32_t)(item % p.num_kv_heads);
+  const int32_t entry = q8_table_entry(p, 0, b, 0, 1);
   const int32_t L = checked_len(p, b, g == 0 && lane == 0);
   if (L == 0) {
     T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_heads + (size_t)g * p.group) * D;
@@ -640,7 +662,7 @@ decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, 
   }
   __syncwarp();
   uint32_t phase = 0;
-  decode_q8_partition<T, D, NT, Code, 1>(tmap, p, lay, smem, ring_bytes, sh, 0, g, b, L, phase);
+  decode_q8_partition<T, D, NT, Code, 1>(tmap, p, lay, smem, ring_bytes, sh, 0, g, b, L, entry, phase);
 }
 
 // Merge of the partition states of one sequence: 4 warps per CTA, grid (H /
