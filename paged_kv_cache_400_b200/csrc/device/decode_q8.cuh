@@ -665,21 +665,23 @@ decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, 
   decode_q8_partition<T, D, NT, Code, 1>(tmap, p, lay, smem, ring_bytes, sh, 0, g, b, L, entry, phase);
 }
 
-// Merge of the partition states of one sequence: 4 warps per CTA, grid (H /
-// kHeads, B). kHeads > 1: a warp takes a head at a time (few partitions, or
-// few CTAs would have anything to do). kHeads == 1: the warps share a head's
-// partitions and join through shared memory. Bound by the latency of a few
+// Merge of the partition states of one sequence. kSplit (many partitions): a
+// CTA of 8 warps per head, which share its partitions and join through shared
+// memory. Otherwise: a CTA of 4 warps per KV head, a warp takes a head at a time. Bound by the latency of a few
 // dependent L2 reads: a warp has 8 partitions' accumulators in flight. Every
 // CTA waits for the partition kernel first, also one with nothing to merge, so
 // that this grid never completes before that one.
-constexpr int kQ8MergeWarps = 4;
+
+template <bool kSplit>
+constexpr int kQ8MergeWarps = kSplit ? 8 : 4;
 
 template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kQ8MergeWarps * 32) decode_q8_merge_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(kQ8MergeWarps<kSplit> * 32) decode_q8_merge_kernel(DecodeParams p) {
+  constexpr int kWarps = kQ8MergeWarps<kSplit>;
   constexpr int E = D / 32;  // output elements per lane
   using Acc = Vec<float, E>;
-  __shared__ float sh_ml[kQ8MergeWarps][2];
-  __shared__ Acc sh_acc[kSplit ? kQ8MergeWarps : 1][32];
+  __shared__ float sh_ml[kWarps][2];
+  __shared__ Acc sh_acc[kSplit ? kWarps : 1][32];
   const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t b = blockIdx.y;
   const int32_t L = checked_len(p, b, false);
@@ -687,19 +689,28 @@ __global__ void __launch_bounds__(kQ8MergeWarps * 32) decode_q8_merge_kernel(Dec
   grid_dependency_wait();
   if (nparts <= 1) return;  // finished by the partition kernel
   const int32_t heads = kSplit ? 1 : p.group;
-  for (int32_t h = kSplit ? 0 : warp; h < heads; h += kSplit ? 1 : kQ8MergeWarps) {
+  for (int32_t h = kSplit ? 0 : warp; h < heads; h += kSplit ? 1 : kWarps) {
     const size_t bh = (size_t)b * p.num_heads + (size_t)blockIdx.x * heads + h;
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + bh * p.max_partitions;
     const Acc* acc = reinterpret_cast<const Acc*>(p.ws_acc) + bh * p.max_partitions * 32 + lane;
-    // chunks of 32 partitions, this warp's first and the stride to its next
-    const int32_t c0 = kSplit ? warp * 32 : 0, step = kSplit ? kQ8MergeWarps * 32 : 32;
+    // chunks of partitions, this warp's first and the stride to its next
+    constexpr int32_t kChunk = kSplit ? 16 : 32;
+    const int32_t c0 = kSplit ? warp * kChunk : 0, step = kSplit ? kWarps * kChunk : kChunk;
     float M = kQ8NoRef, l = 0.f;
     Acc a;
 #pragma unroll
     for (int e = 0; e < E; ++e) a.v[e] = 0.f;
     for (int32_t q0 = c0; q0 < nparts; q0 += step) {
-      const int32_t cnt = min(32, nparts - q0);
+      const int32_t cnt = min(kChunk, nparts - q0);
+      // the first accumulators are asked for together with the references
+      Acc x[8];
+      auto load = [&](int32_t q) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q + j < cnt) x[j] = load_cg(acc + (size_t)(q0 + q + j) * 32);
+      };
       const float2 s = lane < cnt ? __ldcg(ml + q0 + lane) : make_float2(kQ8NoRef, 0.f);
+      load(0);
       float m = s.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -710,10 +721,7 @@ __global__ void __launch_bounds__(kQ8MergeWarps * 32) decode_q8_merge_kernel(Dec
 #pragma unroll
       for (int e = 0; e < E; ++e) a.v[e] *= old;
       for (int32_t q = 0; q < cnt; q += 8) {
-        Acc x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (q + j < cnt) x[j] = load_cg(acc + (size_t)(q0 + q + j) * 32);
+        if (q > 0) load(q);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float wj = __shfl_sync(0xffffffffu, w, (q + j) & 31);
@@ -733,7 +741,7 @@ __global__ void __launch_bounds__(kQ8MergeWarps * 32) decode_q8_merge_kernel(Dec
       __syncthreads();
       if (warp > 0) return;
 #pragma unroll
-      for (int w = 1; w < kQ8MergeWarps; ++w) {
+      for (int w = 1; w < kWarps; ++w) {
         const float m = fmaxf(M, sh_ml[w][0]);
         const float f0 = exp2f(M - m), f1 = exp2f(sh_ml[w][0] - m);
         M = m;
@@ -756,7 +764,7 @@ template <typename T, int D, bool kSplit>
 inline cudaError_t launch_decode_q8_merge(const DecodeParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kSplit ? p.num_heads : p.num_kv_heads, p.num_seqs);
-  cfg.blockDim = dim3(kQ8MergeWarps * 32);
+  cfg.blockDim = dim3(kQ8MergeWarps<kSplit> * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
