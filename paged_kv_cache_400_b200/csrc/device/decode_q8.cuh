@@ -44,10 +44,15 @@
 // fp32 queries: q (scaled per head by a power of two) and P are split into two
 // fp16 terms each (22 significand bits), each term its own MMA.
 //
-// Staging, work list and // Staging and work list are those of decode_staged.cuh:: a ring of
-// TMA boxes per warp (here one box of K and V per block), one CTA per
-// (partition, KV head, sequence) or, from kWorkListPartitions on, resident CTAs
-// that take them from the plan's list; a merge kernel joins them.
+// Staging, work list and // Staging and work list are those of decode_staged.cuh: a ring of TMA boxes per
+// warp, here one box of K and V per block; one CTA per (partition, KV head,
+// sequence), or resident CTAs that take them from the plan kernel's list, or a
+// warp per (sequence, KV head); a merge kernel joins the partitions.
+//
+// Measured: 256 requests of lognormal lengths (32 heads over 8, int8) 124 us,
+// 5.8 TB/s of the pool's bytes; 64 requests with 32 KV heads, e4m3, 99 us, 6.4
+// TB/s, as much as a copy reaches. What is left in the first is the launches of
+// plan and merge (8 us) and the ends of the items.
 #pragma once
 
 #include <algorithm>
@@ -774,39 +779,43 @@ inline cudaError_t launch_decode_q8_merge(const DecodeParams& p, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, decode_q8_merge_kernel<T, D, kSplit>, p);
 }
 
-// Tokens of a partition, a multiple of 16 in [128, 2048]: the resident CTAs
-// (q8_resident) take kQ8Rounds partitions each, or the smallest
-// multiple of that with which 2048 tokens are enough, when every sequence has
-// the longest length.
-#ifndef PA_Q8_ROUNDS
-#define PA_Q8_ROUNDS 1
-#endif
-constexpr int kQ8Rounds = PA_Q8_ROUNDS;
-#ifndef PA_Q8_WARP_PAIRS
-#define PA_Q8_WARP_PAIRS 3
-#endif
+// CTAs that are resident at once (where a group has up to 8 heads).
 inline int32_t q8_resident(int32_t head_dim) {
   return (head_dim == 128 ? Q8Tile<128>::kCtasPerSm : Q8Tile<64>::kCtasPerSm) * device_sm_count();
 }
+// A warp per (sequence, KV head) where sequences are short and pairs many: 200
+// sequences x 8 heads of up to 137 tokens take 10.5 us by warps and 23.8 us by
+// CTAs. With fewer than three pairs per SM the warps are too few to fill it (82
+// x 8 heads of 90 tokens, 4.4 per SM: 10.4 and 14.1 us).
 inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
-  return max_seq_len <= kQ8WarpTokens && pairs >= (int64_t)PA_Q8_WARP_PAIRS * device_sm_count();
+  return max_seq_len <= kQ8WarpTokens && pairs >= (int64_t)3 * device_sm_count();
 }
+// Tokens of a partition, a multiple of 16, at most 2048: when every sequence
+// has the longest length, the resident CTAs take one partition each, or as many
+// as 2048 tokens make necessary (one request of 131071 tokens and 8 heads: two
+// rounds of 1184 tokens, 55 us; three rounds 60 us). Up to 256 tokens, four
+// blocks a warp, a partition is the sequence: the launch that merges costs more
+// (230 tokens: 5.9 us, in two partitions 6.3 us). Two rounds throughout were
+// slower on batches of even lengths (6 x 8 heads of 2928 tokens: 15.0 us by one
+// round, 19.1 by two) and faster on ragged ones (28 x 2 of up to 10517: 23.0 and
+// 18.7 us).
 inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
   const int64_t pairs = std::max<int64_t>((int64_t)num_seqs * num_kv_heads, 1);
   if (q8_by_warp(pairs, max_seq_len)) return kQ8WarpTokens;  // one partition
-  const int64_t resident = (int64_t)q8_resident(head_dim) * kQ8Rounds;
+  const int64_t resident = q8_resident(head_dim);
   const int64_t least = ((int64_t)max_seq_len + 2047) / 2048;  // partitions a sequence needs
   const int64_t rounds = std::max<int64_t>((least * pairs + resident - 1) / resident, 1);
   const int64_t parts = std::max<int64_t>(rounds * resident / pairs, 1);
   const int64_t tokens = (((int64_t)max_seq_len + parts - 1) / parts + 15) / 16 * 16;
-  return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, 128), 2048);
+  const int64_t smallest = max_seq_len <= 256 ? 256 : 128;
+  return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, smallest), 2048);
 }
-
-#ifndef PA_Q8_LIST_ROUNDS
-#define PA_Q8_LIST_ROUNDS 3
-#endif
+// The plan kernel's list from more than three rounds of CTAs on: it saves the
+// empty CTAs of ragged batches and starts the longest partitions first, but is a
+// launch more (182 x 2 heads of 4608 tokens, 2.5 rounds: 80.3 us without, 84.5
+// with it).
 inline bool q8_use_list(int64_t pairs, int32_t partitions, int32_t head_dim) {
-  return partitions >= 2 && pairs * partitions > (int64_t)PA_Q8_LIST_ROUNDS * q8_resident(head_dim);
+  return partitions >= 2 && pairs * partitions > (int64_t)3 * q8_resident(head_dim);
 }
 
 // Tensor map of an 8-bit pool's codes: (byte of a 128-byte line, line of the
