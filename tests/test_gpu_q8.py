@@ -313,6 +313,94 @@ def test_decode_bad_blocks_and_lengths(code, max_len):
     assert torch.equal(out2[1], out[1]) and torch.isfinite(out2).all()
 
 
+@CODE
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("heads_kv,group,dim", [(8, 2, 128), (8, 1, 64), (8, 9, 128)])
+def test_decode_large_ragged_batch(heads_kv, group, dim, io, code):
+    """More partitions than three rounds of CTAs: the list of the plan kernel, empty sequences among them."""
+    r = np.random.RandomState(2)
+    lens = r.randint(0, 40, 300)
+    lens[[3, 77, 150, 299]] = [2100, 2049, 2048, 4000]
+    check_decode(heads_kv, group, dim, code, io, lens.tolist(), max_len=4096, seed=6)
+
+
+@CODE
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_many_short_sequences(dim, io, code):
+    """A warp for each sequence and KV head: lengths over the ring's stages, empty and longest ones."""
+    r = np.random.RandomState(3)
+    lens = r.randint(0, 70, 130)
+    lens[:6] = [0, 1, 512, 511, 497, 64]
+    check_decode(4, 3, dim, code, io, lens.tolist(), max_len=512, seed=7)
+    check_decode(4, 9, dim, code, io, np.minimum(lens, 30).tolist(), max_len=30, seed=8)
+
+
+@CODE
+@pytest.mark.parametrize("max_len", [200, 3000])
+def test_decode_scale_of_any_sign(code, max_len):
+    lens = [40, 200, 1, 17]
+    p = make_pool(30, 2, 64, code, 4)
+    tables = tables_for(lens, 30, (max_len + 15) // 16)
+    codes, scales = host(p)
+    q = rows(4, 8, 64, "bf16", 3)
+    for scale in (-0.2, 0.0, 5.0):
+        out = decode(p, q, tables, lens, max_len, scale)
+        assert pk.pa_get_device_error() == 0
+        check_rows(out, q, lens, [1] * 4, range(4), codes, scales, tables, p, "bf16", scale, 2.0 ** -11, 200,
+                   biased=biased(code, "bf16"))
+
+
+@CODE
+@pytest.mark.parametrize("max_len", [200, 3000])
+def test_decode_non_finite_queries_stay_in_their_head(code, max_len):
+    lens = [40, 200, 1, 17]
+    p = make_pool(30, 2, 64, code, 4)
+    tables = tables_for(lens, 30, (max_len + 15) // 16)
+    q = rows(4, 8, 64, "f32", 3)
+    want = decode(p, q, tables, lens, max_len, 0.1)
+    q[1, 2, 5], q[3, 7, 0], q[0, 4, 1] = float("nan"), float("inf"), -float("inf")
+    got = decode(p, q, tables, lens, max_len, 0.1)
+    hit = torch.zeros(4, 8, dtype=torch.bool)
+    hit[1, 2] = hit[3, 7] = hit[0, 4] = True
+    assert torch.equal(got[~hit], want[~hit]) and not torch.isfinite(got[hit]).all(-1).any()
+    assert pk.pa_get_device_error() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Two requests' steps side by side, each with buffers and a workspace of its own."""
+    lens = [3000, 70, 1500, 900]
+    sets = []
+    for i in range(2):
+        p = make_pool(400, 4, 128, "int8", 20 + i)
+        sets.append((p, torch.from_numpy(tables_for(lens, 400, 188, i)).to(DEV), rows(4, 16, 128, "bf16", 30 + i).to(DEV),
+                     rows(40, 4, 128, "bf16", 40 + i).to(DEV), pk.alloc_workspace(4, 16, p, 3008), torch.cuda.Stream()))
+    dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    slots = torch.arange(16 * 399 - 24, 16 * 400 - 24, device=DEV).repeat(3)[:40]
+
+    def step(s, n):
+        p, t, q, k, ws, _ = s
+        outs = []
+        for _ in range(n):
+            pk.pa_reshape_and_cache_q8(k, k, p, slots)
+            o = torch.empty_like(q)
+            pk.pa_decode_q8(o, q, p, t, dl, 0.09, 3008, ws)
+            outs.append(o)
+        return outs
+
+    torch.cuda.synchronize()
+    want = [step(s, 1)[0] for s in sets]
+    torch.cuda.synchronize()
+    got = []
+    for s in sets:
+        with torch.cuda.stream(s[5]):
+            got.append(step(s, 10))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, o) for o in g)
+    assert pk.pa_get_device_error() == 0
+
+
 def test_decode_high_block_ids():
     """Blocks whose bytes lie behind 2^32."""
     n = (1 << 32) // pk.Q8Pool.block_bytes(8, 128) + 40
