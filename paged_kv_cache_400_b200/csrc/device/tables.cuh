@@ -227,6 +227,17 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, 
   int32_t* c_old = keep ? t.ws_old : cached + t.num_seqs + 1;
   int32_t* c_first = keep ? t.ws_first : cached + 2 * t.num_seqs + 1;
   const int32_t tid = threadIdx.x, lane = tid & 31;
+  // lengths and requests of a pass; the first one's arrive together with the ring's state
+  int32_t L[K], n[K];
+  auto load = [&](int32_t b0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int32_t b = b0 + (tid >> 5) * 32 * K + 32 * k + lane;
+      L[k] = b < t.num_seqs ? t.seq_lens[b] : 0;
+      n[k] = b < t.num_seqs ? t.asked[b] : 0;
+    }
+  };
+  load(0);
   const int32_t head_in = t.state[0], count_in = t.state[1];
   int32_t head = head_in, count = count_in;
   const bool usable = head >= 0 && head < t.ring_size && count >= 0 && count <= t.ring_size;
@@ -241,22 +252,15 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, 
     c_starts[0] = 0;
     if (outputs && kExtend) t.query_start[0] = 0;
   }
-  __syncthreads();
   const uint32_t block_limit = kExtend ? (uint32_t)count : (uint32_t)(t.ring_size - count);
   const uint32_t token_limit = kExtend && t.row_tokens == 0 ? (uint32_t)t.num_slots : kTablesCap;
   const int64_t room = (int64_t)t.width * 16;
   uint32_t blocks0 = 0, tokens0 = 0, granted0 = 0;  // sums over the earlier passes' requests
   bool clean = true;                                // nothing refused so far
   for (int32_t b0 = 0; b0 < t.num_seqs; b0 += K * kTablesThreads) {
-    int32_t L[K], n[K];
+    if (b0 > 0) load(b0);
     uint32_t v[2][K], take[K], sum[2];
     bool bad[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int32_t b = b0 + (tid >> 5) * 32 * K + 32 * k + lane;
-      L[k] = b < t.num_seqs ? t.seq_lens[b] : 0;
-      n[k] = b < t.num_seqs ? t.asked[b] : 0;
-    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (kExtend) {
