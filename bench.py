@@ -215,7 +215,7 @@ DECODE_KERNEL_SOURCES = ("common.cuh", "decode_common.cuh", "decode_staged.cuh",
 
 
 PREFILL_KERNEL_SOURCES = ("common.cuh", "ptx.cuh", "tcgen05.cuh", "decode_common.cuh", "decode_staged.cuh",
-                          "prefill_common.cuh", "prefill_tc.cuh")
+                          "prefill_common.cuh", "prefill_tc.cuh", "q8_common.cuh")
 
 
 def kernel_source_digest(sources=None):

@@ -168,7 +168,7 @@ def library_path() -> str:
 
 
 def _check(fn: str, status: int):
-    if status != PA_OK:
+    if status:  # not PA_OK
         detail = lib().pa_last_error().decode(errors="replace")
         raise PagedKVError(fn, status, detail)
 
@@ -440,7 +440,7 @@ def _current_device(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
@@ -540,14 +540,16 @@ def make_free_ring(num_blocks: int, order=None, device="cuda"):
     return ring.to(device), torch.tensor([0, num_blocks, 0, 0], dtype=torch.int32, device=device)
 
 
-def _tables_args(block_tables, seq_lens, asked, name, seq_lens_out, ring_state, ring_state_out):
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    if B < 0 or block_tables.dim() != 2 or block_tables.shape[0] != B or asked.shape != (B,) \
-            or seq_lens_out.shape != (B,):
+def _tables_args(block_tables, seq_lens, asked, name, seq_lens_out, ring_state, ring_state_out, free_ring):
+    """(num_seqs, max_blocks_per_seq, ring_size) of well-shaped arguments."""
+    one, two, ring = seq_lens.shape, block_tables.shape, free_ring.shape
+    if len(one) != 1 or len(two) != 2 or two[0] != one[0] or asked.shape != one or seq_lens_out.shape != one:
         raise ValueError(f"block_tables [num_seqs][max_blocks]; seq_lens, {name}, seq_lens_out [num_seqs]")
     if ring_state.numel() < 2 or ring_state_out.shape != (4,):
         raise ValueError("ring_state holds head and count, ring_state_out [4]")
-    return B
+    if len(ring) != 1:
+        raise ValueError("free_ring [ring_size]")
+    return one[0], two[1], ring[0]
 
 
 def pa_tables_extend(block_tables, seq_lens, new_tokens, free_ring, ring_state, seq_lens_out, query_start,
@@ -555,18 +557,20 @@ def pa_tables_extend(block_tables, seq_lens, new_tokens, free_ring, ring_state, 
     """Gives each request its new_tokens next tokens: takes their blocks from
     the free ring, extends block_tables in place, and writes the new lengths,
     query_start and the tokens' slots (packed, or row_tokens per request)."""
-    B = _tables_args(block_tables, seq_lens, new_tokens, "new_tokens", seq_lens_out, ring_state, ring_state_out)
-    if query_start.shape != (B + 1,) or slot_mapping.dim() != 1 or free_ring.dim() != 1:
-        raise ValueError("query_start [num_seqs + 1], slot_mapping [num_slots], free_ring [ring_size]")
+    B, width, ring_size = _tables_args(block_tables, seq_lens, new_tokens, "new_tokens", seq_lens_out, ring_state,
+                                       ring_state_out, free_ring)
+    slots = slot_mapping.shape
+    if query_start.shape != (B + 1,) or len(slots) != 1:
+        raise ValueError("query_start [num_seqs + 1], slot_mapping [num_slots]")
     if workspace is None:
         workspace = alloc_tables_workspace(B, seq_lens.device)
     dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
     _check("pa_tables_extend", lib().pa_tables_extend(
-        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i),
-        _here(new_tokens, "new_tokens", dev, i), B, _here(free_ring, "free_ring", dev, i), free_ring.shape[0],
+        _here(block_tables, "block_tables", dev, i), width, _here(seq_lens, "seq_lens", dev, i),
+        _here(new_tokens, "new_tokens", dev, i), B, _here(free_ring, "free_ring", dev, i), ring_size,
         _here(ring_state, "ring_state", dev, i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", dev, i),
         _here(query_start, "query_start", dev, i), _here(slot_mapping, "slot_mapping", dev, torch.int64),
-        slot_mapping.shape[0], int(row_tokens), _here(ring_state_out, "ring_state_out", dev, i),
+        slots[0], int(row_tokens), _here(ring_state_out, "ring_state_out", dev, i),
         _here(workspace, "workspace", dev, workspace.dtype), workspace.nbytes, _launch_stream(stream, dev)))
 
 
@@ -574,15 +578,14 @@ def pa_tables_release(block_tables, seq_lens, finished, free_ring, ring_state, s
                       num_blocks, workspace=None, stream=None):
     """Gives the blocks of every request with finished[b] != 0 back to the free
     ring (in place) and sets its length to 0."""
-    B = _tables_args(block_tables, seq_lens, finished, "finished", seq_lens_out, ring_state, ring_state_out)
-    if free_ring.dim() != 1:
-        raise ValueError("free_ring [ring_size]")
+    B, width, ring_size = _tables_args(block_tables, seq_lens, finished, "finished", seq_lens_out, ring_state,
+                                       ring_state_out, free_ring)
     if workspace is None:
         workspace = alloc_tables_workspace(B, seq_lens.device)
     dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
     _check("pa_tables_release", lib().pa_tables_release(
-        _here(block_tables, "block_tables", dev, i), block_tables.shape[1], _here(seq_lens, "seq_lens", dev, i),
-        _here(finished, "finished", dev, i), B, _here(free_ring, "free_ring", dev, i), free_ring.shape[0],
+        _here(block_tables, "block_tables", dev, i), width, _here(seq_lens, "seq_lens", dev, i),
+        _here(finished, "finished", dev, i), B, _here(free_ring, "free_ring", dev, i), ring_size,
         _here(ring_state, "ring_state", dev, i), int(num_blocks), _here(seq_lens_out, "seq_lens_out", dev, i),
         _here(ring_state_out, "ring_state_out", dev, i), _here(workspace, "workspace", dev, workspace.dtype),
         workspace.nbytes, _launch_stream(stream, dev)))
