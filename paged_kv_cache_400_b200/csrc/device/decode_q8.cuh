@@ -550,30 +550,45 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   }
   __syncthreads();
 
-  T* out = reinterpret_cast<T*>(p.out);
-  for (int32_t i = threadIdx.x; i < G * D; i += blockDim.x) {
-    const int32_t h = i / D;
-    const int32_t d = i % D;
+  // each head's weights of the four warps, divided by the sum where this is the output
+  if (threadIdx.x < G) {
+    const int32_t h = threadIdx.x;
     float M = kQ8NoRef;
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sh.red_m[w][h]);
-    float Ls = 0.f, A = 0.f;
+    float e[kQ8Warps], Ls = 0.f;
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) {
-      const float e = exp2f(sh.red_m[w][h] - M);  // 0 for a warp that had no block
-      Ls = fmaf(sh.red_l[w][h], e, Ls);
-      A = fmaf(so[(w * 8 * NT + h) * kRow + d], e, A);
+      e[w] = exp2f(sh.red_m[w][h] - M);  // 0 for a warp that had no block
+      Ls = fmaf(sh.red_l[w][h], e[w], Ls);
+    }
+    const float f = nparts == 1 ? 1.f / Ls : 1.f;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) sh.red_m[w][h] = e[w] * f;
+    if (nparts > 1)
+      reinterpret_cast<float2*>(p.ws_ml)[((size_t)b * H + (size_t)g * G + h) * p.max_partitions + part] =
+          make_float2(M, Ls);
+  }
+  __syncthreads();
+  T* out = reinterpret_cast<T*>(p.out);
+  for (int32_t i = threadIdx.x; i < G * (D / 4); i += blockDim.x) {
+    const int32_t h = i / (D / 4), d = i % (D / 4) * 4;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * kRow + d);
+      const float e = sh.red_m[w][h];
+      A.x = fmaf(x.x, e, A.x);
+      A.y = fmaf(x.y, e, A.y);
+      A.z = fmaf(x.z, e, A.z);
+      A.w = fmaf(x.w, e, A.w);
     }
     const size_t bh = (size_t)b * H + (size_t)g * G + h;
-    if (nparts == 1) {
-      out[bh * D + d] = Elem<T>::from_f32(A / Ls);
-    } else {
-      p.ws_acc[(bh * p.max_partitions + part) * D + d] = A;
-      if (d == 0) {
-        p.ws_ml[(bh * p.max_partitions + part) * 2] = M;
-        p.ws_ml[(bh * p.max_partitions + part) * 2 + 1] = Ls;
-      }
-    }
+    if (nparts == 1)
+      *reinterpret_cast<Vec<T, 4>*>(out + bh * D + d) = {Elem<T>::from_f32(A.x), Elem<T>::from_f32(A.y),
+                                                         Elem<T>::from_f32(A.z), Elem<T>::from_f32(A.w)};
+    else
+      *reinterpret_cast<float4*>(p.ws_acc + (bh * p.max_partitions + part) * D + d) = A;
   }
 }
 
