@@ -49,8 +49,8 @@
 // sequence), or resident CTAs that take them from the plan kernel's list, or a
 // warp per (sequence, KV head); a merge kernel joins the partitions.
 //
-// Measured: 256 requests of lognormal lengths (32 heads over 8, int8) 124 us,
-// 5.8 TB/s of the pool's bytes; 64 requests with 32 KV heads, e4m3, 99 us, 6.4
+// Measured: 256 requests of lognormal lengths (32 heads over 8, int8) 121 us,
+// 5.9 TB/s of the pool's bytes; 64 requests with 32 KV heads, e4m3, 99 us, 6.4
 // TB/s, as much as a copy reaches. What is left in the first is the launches of
 // plan and merge (8 us) and the ends of the items.
 #pragma once
@@ -808,7 +808,7 @@ inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
 // Tokens of a partition, a multiple of 16, at most 2048: when every sequence
 // has the longest length, the resident CTAs take one partition each, or as many
 // as 2048 tokens make necessary (one request of 131071 tokens and 8 heads: two
-// rounds of 1184 tokens, 55 us; three rounds 60 us). Up to 256 tokens, four
+// rounds of 1184 tokens, 54 us; three rounds 60 us). Up to 256 tokens, four
 // blocks a warp, a partition is the sequence: the launch that merges costs more
 // (230 tokens: 5.9 us, in two partitions 6.3 us). Two rounds throughout were
 // slower on batches of even lengths (6 x 8 heads of 2928 tokens: 15.0 us by one
