@@ -813,7 +813,12 @@ inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
 // (230 tokens: 5.9 us, in two partitions 6.3 us). Two rounds throughout were
 // slower on batches of even lengths (6 x 8 heads of 2928 tokens: 15.0 us by one
 // round, 19.1 by two) and faster on ragged ones (28 x 2 of up to 10517: 23.0 and
-// 18.7 us).
+// 18.7 us). Batches of three to ten rounds of 2048 tokens, taken from the list,
+// get 1024: their lengths are ragged as a rule, and the longest items would end
+// alone (64 x 8 heads, lognormal up to 8192: 42.8 us, by 2048 tokens 51.7; all of
+// 8192: 174.5 and 174.8). Beyond ten rounds 2048 are enough and cheaper (256 x 8:
+// 121 us, by 1024 tokens 130), and sequences that fit one partition are not cut
+// (64 x 32 of up to 2048: 99 and 106 us).
 inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
   const int64_t pairs = std::max<int64_t>((int64_t)num_seqs * num_kv_heads, 1);
   if (q8_by_warp(pairs, max_seq_len)) return kQ8WarpTokens;  // one partition
@@ -823,7 +828,9 @@ inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32
   const int64_t parts = std::max<int64_t>(rounds * resident / pairs, 1);
   const int64_t tokens = (((int64_t)max_seq_len + parts - 1) / parts + 15) / 16 * 16;
   const int64_t smallest = max_seq_len <= 256 ? 256 : 128;
-  return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, smallest), 2048);
+  const bool some_rounds = pairs * least > 3 * resident && pairs * least <= 10 * resident;
+  const int64_t most = least > 1 && some_rounds ? 1024 : 2048;
+  return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, smallest), most);
 }
 // The plan kernel's list from more than three rounds of CTAs on: it saves the
 // empty CTAs of ragged batches and starts the longest partitions first, but is a
