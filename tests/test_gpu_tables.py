@@ -189,6 +189,46 @@ def test_release_bad_requests():
     check_release([20, 33], [1, 1], 4, 40, head=39, count=41)
 
 
+@pytest.mark.parametrize("batch,row", [(40, 1), (700, 4), (2500, 3), (5000, 1)])
+def test_captured_steps_in_place(batch, row):
+    """Lengths and ring advanced in place by a replayed graph (one launch, two launches, sums in the
+    workspace), then released by another that shares the workspace."""
+    W, N = 4, batch * 4
+    r = np.random.RandomState(batch)
+    t, ring, h, c = make(np.zeros(batch, int), W, N, batch)
+    o_t, o_l, o_r = t.tolist(), [0] * batch, ring.tolist()
+    dt, dl, dr, ds = i32(t).reshape(batch, W), i32([0] * batch), i32(ring), i32([h, c, 0, 0])
+    ask, qs = i32([0] * batch), i32([0] * (batch + 1))
+    slots = torch.zeros(batch * row, dtype=torch.int64, device=DEV)
+    ws = pk.alloc_tables_workspace(batch)
+    up = lambda: pk.pa_tables_extend(dt, dl, ask, dr, ds, dl, qs, slots, ds, N, row, ws)
+    down = lambda: pk.pa_tables_release(dt, dl, ask, dr, ds, dl, ds, N, ws)
+    up(), down()  # nothing asked for: no state changes
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (up, down):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    for step in range(6):
+        if step == 3:
+            done = (r.rand(batch) < 0.4).astype(int).tolist()
+            ask.copy_(torch.tensor(done, dtype=torch.int32))
+            graphs[1].replay()
+            o_l, st, err = ot.release(o_t, o_l, done, o_r, h, c, N)
+        else:
+            new = r.randint(0, row + 1, batch).tolist()
+            ask.copy_(torch.tensor(new, dtype=torch.int32))
+            graphs[0].replay()
+            o_l, start, o_s, st, err = ot.extend(o_t, o_l, new, o_r, h, c, N, batch * row, row)
+            assert slots.tolist() == o_s and qs.tolist() == start
+        h, c = st[:2]
+        assert err == 0 and dl.tolist() == o_l and ds.tolist() == st and dr.tolist() == o_r
+        assert dt.tolist() == o_t
+    assert pk.pa_get_device_error() == 0
+
+
 def test_same_blocks_as_the_host_block_manager():
     """Requests come, grow and leave: tables, lengths and slots stay the host block manager's."""
     r = np.random.RandomState(0)
