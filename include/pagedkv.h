@@ -353,8 +353,9 @@ int64_t pa_pool_block_bytes(pa_pool_desc pool);
  *       entries of the block's one before (padding may lie between, and order
  *       does not matter), are written together; of two with the same slot the
  *       later one is stored. A block may come back after a longer gap only with
- *       the rows and values it had before, as when requests that share a prefix
- *       are admitted in one step: it is then written twice at the same time.
+ *       the rows and values it had before and row 0 among them, as when
+ *       requests that share a prefix are admitted in one step: it is then
+ *       written twice at the same time, with the same bytes.
  */
 pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool,
                                   const int64_t* slot_mapping, int32_t num_tokens,
@@ -368,8 +369,10 @@ size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads,
  * pa_decode over an 8-bit pool: the same operation, arguments, checks and
  * errors, with K_t and V_t = code * scale. q, out: io_dtype. Products are
  * formed on the codes (exact in fp16) and accumulated in fp32; bf16 queries
- * are exact too, probabilities are rounded to fp16 (2^-11 relative); fp32
- * queries and their probabilities keep 22 bits.
+ * are exact too (down to 2^-31 of a head's largest element), probabilities are
+ * rounded to fp16 (2^-11 relative); fp32 queries and their probabilities keep
+ * 22 bits. int8 codes of bf16 queries are summed as code + 128 and the 128s
+ * taken off in fp32.
  */
 pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
                        const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -383,8 +386,9 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
  * errors, with K_t and V_t = code * scale; q, out bf16. Products are formed on
  * the codes (exact in bf16 and fp16) and accumulated in fp32; a probability
  * times its V scale is rounded to fp16 (2^-11 relative). Where scores pass about
- * 2^25 (off by units in fp32) a row may come out as 0. Supported: head_dim 128, num_heads / num_kv_heads in
- * {1, 2, 4, 8, 16}, scale >= 0 (else PA_ERR_INVALID_ARG).
+ * 2^25 (off by units in fp32) a row may come out as 0. Supported: head_dim 128,
+ * num_heads / num_kv_heads in {1, 2, 4, 8, 16}, scale >= 0 (else
+ * PA_ERR_INVALID_ARG).
  */
 pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,
                         const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -402,9 +406,10 @@ pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool,
  * - 1 (modulo ring_size) are free, the head first ([C] §2.2 keeps the free
  * blocks in a deque). A ring_size of num_blocks holds any state. The calls
  * write int32 [4] {head, count, tokens, refused}: `tokens` the tokens granted
- * (0 by release), `refused` the requests that asked and got nothing. Blocks are taken and given back in request and table order,
- * as pa_bm_allocate, pa_bm_append_slot and pa_bm_free do for one sequence after
- * another, so tables and slots are the host block manager's. The requests own
+ * (0 by release), `refused` the requests that asked and got nothing. Blocks are
+ * taken and given back in request and table order, as pa_bm_allocate,
+ * pa_bm_append_slot and pa_bm_free do for one sequence after another, so tables
+ * and slots are the host block manager's. The requests own
  * their blocks alone: the calls know no shared blocks (fork and copy-on-write
  * stay with the host block manager).
  * Each output may be the matching input (seq_lens_out = seq_lens,

@@ -13,8 +13,8 @@
 // entries of the one before; these lead nothing. A row named twice takes the
 // later token. A block that comes back after a longer gap has a second leader,
 // which writes at the same time: requests that share a prefix and are admitted
-// in one step name its blocks with the same rows and values, so both store the
-// same bytes.
+// in one step name its whole blocks with the same values, so both start the
+// tile afresh and store the same bytes.
 //
 // Bound by its bytes (reads T * Hkv * D elements twice over for K and V, writes
 // half or a quarter as many) for many tokens, by latency for few. A warp looks

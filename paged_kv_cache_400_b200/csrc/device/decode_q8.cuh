@@ -24,9 +24,8 @@
 //    int8, bf16 queries: the subtraction is put off; the bytes code + 128 stand
 //    in fp16's subnormals, u 2^-24, and 128 times the sum of the queries, or of
 //    the probabilities (one more MMA, against ones), comes off the fp32 sums.
-//    That costs 8 bits of those sums' headroom, against 5 bits that bf16 and
-//    the fp16 probabilities leave unused, and saves a quarter of the block's
-//    instructions.
+//    The sums then err by up to 255 parts in 2^24 of a code for each term, where
+//    the probabilities' rounding is 2^-11; a block takes 64 instructions less.
 //  * The reference a head's exponentials are taken against rises only when an
 //    exponent exceeds it by more than 8, which one warp vote finds out; the
 //    shuffles of a true running maximum are left out of the common block.
@@ -44,7 +43,7 @@
 // fp32 queries: q (scaled per head by a power of two) and P are split into two
 // fp16 terms each (22 significand bits), each term its own MMA.
 //
-// Staging, work list and // Staging and work list are those of decode_staged.cuh: a ring of TMA boxes per
+// Staging and work list are those of decode_staged.cuh: a ring of TMA boxes per
 // warp, here one box of K and V per block; one CTA per (partition, KV head,
 // sequence), or resident CTAs that take them from the plan kernel's list, or a
 // warp per (sequence, KV head); a merge kernel joins the partitions.
@@ -295,7 +294,8 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
 
   float o[KK][NT][4];
   float ps[NT][4];                     // kBias: the sums of the P that o is made of
-  float m[NT][2], r[NT][2], l[NT][2];  // reference m + r and sum, heads 8 nt + 2 tig (+ 1); o, l in units of 2^(m + r - lift)
+  // reference m + r and sum, heads 8 nt + 2 tig (+ 1); o and l in units of 2^(m + r - lift)
+  float m[NT][2], r[NT][2], l[NT][2];
   bool far = false;                    // some |m| > kQ8Far (the same in the whole warp)
   auto clear = [&]() {
 #pragma unroll
@@ -687,11 +687,11 @@ decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, 
 
 // Merge of the partition states of one sequence. kSplit (many partitions): a
 // CTA of 8 warps per head, which share its partitions and join through shared
-// memory. Otherwise: a CTA of 4 warps per KV head, a warp takes a head at a time. Bound by the latency of a few
-// dependent L2 reads: a warp has 8 partitions' accumulators in flight. Every
-// CTA waits for the partition kernel first, also one with nothing to merge, so
-// that this grid never completes before that one.
-
+// memory. Otherwise: a CTA of 4 warps per KV head, a warp takes a head at a
+// time. Bound by the latency of a few dependent L2 reads: a warp has 8
+// partitions' accumulators in flight. Every CTA waits for the partition kernel
+// first, also one with nothing to merge, so that this grid never completes
+// before that one.
 template <bool kSplit>
 constexpr int kQ8MergeWarps = kSplit ? 8 : 4;
 

@@ -645,8 +645,9 @@ pa_status pa_prefill_q8(void* out, const void* q, const void* kv_pool, const int
   p.scale_log2 = scale * pagedkv::kLog2e;
   p.q8 = pagedkv::q8_layout(pool.num_kv_heads, pool.head_dim);
   cudaStream_t st = (cudaStream_t)stream;
-  return pool.dtype == PA_Q8_INT8 ? pagedkv::launch_prefill_tc<pagedkv::CodeInt8>(kv_pool, pool.num_blocks, p, num_seqs, st)
-                                  : pagedkv::launch_prefill_tc<pagedkv::CodeE4m3>(kv_pool, pool.num_blocks, p, num_seqs, st);
+  if (pool.dtype == PA_Q8_INT8)
+    return pagedkv::launch_prefill_tc<pagedkv::CodeInt8>(kv_pool, pool.num_blocks, p, num_seqs, st);
+  return pagedkv::launch_prefill_tc<pagedkv::CodeE4m3>(kv_pool, pool.num_blocks, p, num_seqs, st);
 }
 
 }  // extern "C"
