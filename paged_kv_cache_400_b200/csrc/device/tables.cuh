@@ -35,9 +35,10 @@ namespace pagedkv {
 constexpr int kTablesCached = 4096;      // requests whose sums a CTA keeps in shared memory
 // 512 threads with 2 requests, or positions, in flight each: a step of 256
 // requests 3.4 us (4 in flight: 4.5, the code and the registers cost more than
-// the latency), 1000 prompts 8.5 us, 4096 released requests 11.7 us (1024
-// threads: 4.6, 8.3 and 10.0 us).
+// the latency; 1024 threads: 3.8), 1000 prompts 8.5 us. From 2048 requests on
+// 1024 threads: 4096 released requests 10.0 us instead of 11.7.
 constexpr int kTablesThreads = 512;
+constexpr int kTablesMostThreads = 1024;
 constexpr int kTablesPerThread = 2;
 constexpr int32_t kTablesMost = 1 << 30;  // entries of a ring, slots
 constexpr uint32_t kTablesCap = 0x7fffffffu;
@@ -216,7 +217,7 @@ __device__ __forceinline__ void tables_positions(const TablesParams& t, int32_t 
 constexpr int kTablesFill = 1, kTablesOutputs = 2, kTablesKeep = 4;
 
 template <bool kExtend>
-__global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, int32_t positions, int32_t per_cta,
+__global__ void __launch_bounds__(kTablesMostThreads) tables_kernel(TablesParams t, int32_t positions, int32_t per_cta,
                                                                 int32_t todo) {
   extern __shared__ int32_t cached[];  // starts [B + 1], old [B], first [B], unless kTablesKeep
   __shared__ uint32_t sums[2][32];
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, 
   const int64_t room = (int64_t)t.width * 16;
   uint32_t blocks0 = 0, tokens0 = 0, granted0 = 0;  // sums over the earlier passes' requests
   bool clean = true;                                // nothing refused so far
-  for (int32_t b0 = 0; b0 < t.num_seqs; b0 += K * kTablesThreads) {
+  for (int32_t b0 = 0; b0 < t.num_seqs; b0 += K * (int32_t)blockDim.x) {
     if (b0 > 0) load(b0);
     uint32_t v[2][K], take[K], sum[2];
     bool bad[K];
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(TablesParams t, 
 
 // The positions from the workspace's sums, after a launch with kTablesKeep.
 template <bool kExtend>
-__global__ void __launch_bounds__(kTablesThreads) tables_fill_kernel(TablesParams t, int32_t positions,
+__global__ void __launch_bounds__(kTablesMostThreads) tables_fill_kernel(TablesParams t, int32_t positions,
                                                                      int32_t per_cta) {
   grid_dependency_wait();
   const int64_t p0 = (int64_t)blockIdx.x * per_cta;
@@ -380,8 +381,8 @@ inline cudaError_t launch_tables(TablesParams t, void* workspace, int64_t positi
   t.ws_first = t.ws_old + t.num_seqs;
   const int32_t n = (int32_t)positions;
   // a position per thread, and more on at most one CTA per SM: each takes the sums for itself
-  constexpr int32_t kTile = kTablesThreads;
-  const int32_t ctas = std::max(1, std::min((n + kTile - 1) / kTile, device_sm_count()));
+  const int32_t threads = t.num_seqs > 2048 ? kTablesMostThreads : kTablesThreads;
+  const int32_t ctas = std::max(1, std::min((n + threads - 1) / threads, device_sm_count()));
   const int32_t per_cta = (n + ctas - 1) / ctas;
   const bool cached = t.num_seqs <= kTablesCached;
   const size_t smem = cached ? (size_t)(kExtend ? 3 : 1) * (t.num_seqs + 1) * sizeof(int32_t) : 0;
@@ -393,7 +394,7 @@ inline cudaError_t launch_tables(TablesParams t, void* workspace, int64_t positi
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kTablesThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   const bool in_place = t.lens_out == t.seq_lens || t.state_out == t.state;
