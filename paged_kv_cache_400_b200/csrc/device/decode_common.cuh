@@ -61,8 +61,11 @@ __device__ __forceinline__ void grid_dependents_launch() {
 // shared memory, each head's weights exp2(m_p - M) / L are formed once, and
 // each output element then sums its partial accumulators with every load of a
 // round in flight together (a few L2 round trips per CTA, not one per
-// partition). Launched as a programmatic dependent of the partition kernel:
-// everything before griddepcontrol.wait may overlap that kernel's tail.
+// partition). Launched as a programmatic dependent of the partition kernel.
+// Every CTA waits for that kernel before it reads anything: with the work list
+// the plan and the partition kernel release their dependents at once, so what
+// wrote the lengths may still run when this grid starts; and a CTA without
+// partitions to merge must not let this grid complete before that kernel.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeMaxParts = 64;
 
@@ -75,10 +78,10 @@ __global__ void __launch_bounds__(kMergeThreads) partition_merge_kernel(DecodePa
   const int32_t g = blockIdx.x;
   const int32_t b = blockIdx.y;
   const int32_t G = p.group;
+  grid_dependency_wait();  // the lengths and the partition kernel's states are complete and visible
   const int32_t L = checked_len(p, b, false);
   const int32_t nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
   if (nparts <= 1) return;  // finished by the partition kernel
-  grid_dependency_wait();   // the partition kernel's states are complete and visible
   const size_t bh0 = (size_t)b * p.num_heads + (size_t)g * G;
   if (nparts <= kMergeMaxParts) {
     for (int32_t i = threadIdx.x; i < G * nparts; i += blockDim.x) {

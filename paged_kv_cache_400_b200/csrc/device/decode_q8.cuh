@@ -690,8 +690,8 @@ decode_q8_warp_kernel(const __grid_constant__ CUtensorMap tmap, DecodeParams p, 
 // memory. Otherwise: a CTA of 4 warps per KV head, a warp takes a head at a
 // time. Bound by the latency of a few dependent L2 reads: a warp has 8
 // partitions' accumulators in flight. Every CTA waits for the partition kernel
-// first, also one with nothing to merge, so that this grid never completes
-// before that one.
+// before it reads anything, the lengths too, and also where it has nothing to
+// merge (see partition_merge_kernel).
 template <bool kSplit>
 constexpr int kQ8MergeWarps = kSplit ? 8 : 4;
 
@@ -704,9 +704,9 @@ __global__ void __launch_bounds__(kQ8MergeWarps<kSplit> * 32) decode_q8_merge_ke
   __shared__ Acc sh_acc[kSplit ? kWarps : 1][32];
   const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t b = blockIdx.y;
+  grid_dependency_wait();
   const int32_t L = checked_len(p, b, false);
   const int32_t nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
-  grid_dependency_wait();
   if (nparts <= 1) return;  // finished by the partition kernel
   const int32_t heads = kSplit ? 1 : p.group;
   for (int32_t h = kSplit ? 0 : warp; h < heads; h += kSplit ? 1 : kWarps) {

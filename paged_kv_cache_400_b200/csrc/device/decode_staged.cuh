@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(128) decode_staged_kernel(const __grid_constan
   const int32_t warp = threadIdx.x >> 5;
   const int32_t lane = threadIdx.x & 31;
   // the partition merge may be scheduled as soon as every CTA has started; it
-  // waits for this grid's completion before reading any partition state
+  // waits for this grid's completion before it reads anything
   grid_dependents_launch();
   int32_t grid_len = 0;
   if (p.work_items == nullptr) {

@@ -213,8 +213,10 @@ __device__ __forceinline__ void tables_positions(const TablesParams& t, int32_t 
 
 // The sums over all requests, and what a launch is asked to do with them:
 // kFill the positions, kOutputs lengths, query_start and state (by the first
-// CTA), kKeep the sums into the workspace (one CTA, any number of requests).
-constexpr int kTablesFill = 1, kTablesOutputs = 2, kTablesKeep = 4;
+// CTA), kKeep the sums into the workspace (one CTA, any number of requests),
+// kMore let the call's second launch start. A call's last launch releases
+// nothing early: what comes after it reads its lengths, tables and slots.
+constexpr int kTablesFill = 1, kTablesOutputs = 2, kTablesKeep = 4, kTablesMore = 8;
 
 template <bool kExtend>
 __global__ void __launch_bounds__(kTablesMostThreads) tables_kernel(TablesParams t, int32_t positions, int32_t per_cta,
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kTablesMostThreads) tables_kernel(TablesParams
   __shared__ uint32_t taken;  // ring entries granted (release: given back)
   __shared__ int32_t refused;
   constexpr int K = kTablesPerThread;
-  grid_dependents_launch();
+  if (todo & kTablesMore) grid_dependents_launch();
   grid_dependency_wait();
   const bool keep = todo & kTablesKeep;
   const bool outputs = (todo & kTablesOutputs) && blockIdx.x == 0;
@@ -401,7 +403,7 @@ inline cudaError_t launch_tables(TablesParams t, void* workspace, int64_t positi
   if (cached && (ctas == 1 || !in_place))
     return cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta, kTablesFill | kTablesOutputs);
   if (cached) {
-    e = cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta, kTablesFill);
+    e = cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta, kTablesFill | kTablesMore);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(1);
     cfg.attrs = attr;
@@ -409,7 +411,8 @@ inline cudaError_t launch_tables(TablesParams t, void* workspace, int64_t positi
     return cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta, kTablesOutputs);
   }
   cfg.gridDim = dim3(1);
-  e = cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta, kTablesOutputs | kTablesKeep);
+  e = cudaLaunchKernelEx(&cfg, tables_kernel<kExtend>, t, n, per_cta,
+                         kTablesOutputs | kTablesKeep | kTablesMore);
   if (e != cudaSuccess || n == 0) return e;
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.attrs = attr;
