@@ -532,6 +532,22 @@ def alloc_tables_workspace(num_seqs: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _tables_workspace(workspace, num_seqs: int, stream, dev: int) -> torch.Tensor:
+    """The caller's workspace, or one that belongs to the stream the call runs
+    on: the kernels may still use it after the call has dropped it, so whoever
+    gets its bytes next has to come behind them on that stream."""
+    if workspace is not None:
+        return workspace
+    if stream is None:
+        return alloc_tables_workspace(num_seqs, dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        # 0 and 1 (cudaStreamLegacy) name the default stream
+        stream = torch.cuda.ExternalStream(handle, dev) if handle > 1 else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return alloc_tables_workspace(num_seqs, dev)
+
+
 def make_free_ring(num_blocks: int, order=None, device="cuda"):
     """(free_ring, ring_state) of a pool whose blocks are all free, handed out
     in `order` (0, 1, ... by default)."""
@@ -563,9 +579,8 @@ def pa_tables_extend(block_tables, seq_lens, new_tokens, free_ring, ring_state, 
     slots = slot_mapping.shape
     if query_start.shape != (B + 1,) or len(slots) != 1:
         raise ValueError("query_start [num_seqs + 1], slot_mapping [num_slots]")
-    if workspace is None:
-        workspace = alloc_tables_workspace(B, seq_lens.device)
     dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
+    workspace = _tables_workspace(workspace, B, stream, dev)
     _check("pa_tables_extend", lib().pa_tables_extend(
         _here(block_tables, "block_tables", dev, i), width, _here(seq_lens, "seq_lens", dev, i),
         _here(new_tokens, "new_tokens", dev, i), B, _here(free_ring, "free_ring", dev, i), ring_size,
@@ -581,9 +596,8 @@ def pa_tables_release(block_tables, seq_lens, finished, free_ring, ring_state, s
     ring (in place) and sets its length to 0."""
     B, width, ring_size = _tables_args(block_tables, seq_lens, finished, "finished", seq_lens_out, ring_state,
                                        ring_state_out, free_ring)
-    if workspace is None:
-        workspace = alloc_tables_workspace(B, seq_lens.device)
     dev, i = _current_device(seq_lens, "seq_lens"), torch.int32
+    workspace = _tables_workspace(workspace, B, stream, dev)
     _check("pa_tables_release", lib().pa_tables_release(
         _here(block_tables, "block_tables", dev, i), width, _here(seq_lens, "seq_lens", dev, i),
         _here(finished, "finished", dev, i), B, _here(free_ring, "free_ring", dev, i), ring_size,
