@@ -349,13 +349,9 @@ int64_t pa_pool_block_bytes(pa_pool_desc pool);
  * tile whose scale is 0), and either sets PA_DEVERR_NONFINITE.
  * k, v: device, [num_tokens][num_kv_heads][head_dim] contiguous, io_dtype,
  *       16-byte aligned.
- * slot_mapping: as pa_reshape_and_cache. A block's tokens, each within 31
- *       entries of the block's one before (padding may lie between, and order
- *       does not matter), are written together; of two with the same slot the
- *       later one is stored. A block may come back after a longer gap only with
- *       the rows and values it had before and row 0 among them, as when
- *       requests that share a prefix are admitted in one step: it is then
- *       written twice at the same time, with the same bytes.
+ * slot_mapping: as pa_reshape_and_cache; the tokens of a block may lie anywhere
+ *       in it, in any order, and are written together. Of two with the same slot
+ *       the later one is stored.
  */
 pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool,
                                   const int64_t* slot_mapping, int32_t num_tokens,

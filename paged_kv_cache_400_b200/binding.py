@@ -468,9 +468,8 @@ def _q8_pool(pool) -> Q8Pool:
 
 def pa_reshape_and_cache_q8(k, v, pool, slot_mapping, stream=None):
     """Codes the rows k, v [num_tokens][num_kv_heads][head_dim] (fp32 or bf16)
-    into their slots of a Q8Pool. A block's tokens lie each within 31 entries of
-    slot_mapping of the one before; a block comes back after a longer gap only
-    whole, with the values it had (a prefix that requests share)."""
+    into their slots of a Q8Pool, in any order; of two with the same slot the
+    later one is stored."""
     pool = _q8_pool(pool)
     n = slot_mapping.numel()
     if k.shape != (n, pool.num_kv_heads, pool.head_dim) or v.shape != k.shape:

@@ -7,29 +7,33 @@
 // new element is stored as the code nearest to x * (1 / s).
 //
 // One warp owns a tile, so a scale and the rows under it change together and
-// nothing is summed or ordered across warps: the warp of a block's first token
-// in slot_mapping (its leader: none of the 31 entries before it names the block)
-// gathers the block's other tokens behind it, as long as each lies within 31
-// entries of the one before; these lead nothing. A row named twice takes the
-// later token. A block that comes back after a longer gap has a second leader,
-// which writes at the same time: requests that share a prefix and are admitted
-// in one step name its whole blocks with the same values, so both start the
-// tile afresh and store the same bytes.
+// nothing is summed or ordered across warps. A block's tokens may lie anywhere
+// in slot_mapping, in any order, and a row named twice takes the later token.
+// So each CTA looks at the whole list for its own few entries: their blocks go
+// into a hash table in shared memory, and every entry of the list that names
+// one of them either says that an earlier CTA leads the block, or is noted as
+// the latest token of its row. The blocks left over are the CTA's, and its warps
+// share their (block, K|V, head) tiles.
 //
 // Bound by its bytes (reads T * Hkv * D elements twice over for K and V, writes
-// half or a quarter as many) for many tokens, by latency for few. A warp looks
-// at a run of entries at once, with the entries before and behind them, and
-// then serves their leaders: the scale and all new rows of a tile are in flight
-// together, 16 bytes a lane, and stay in registers between the maximum and the
-// codes.
+// half or a quarter as many) for many tokens, by latency for few. The scale and
+// all new rows of a tile are in flight together, 16 bytes a lane, and stay in
+// registers between the maximum and the codes: up to 124 a thread (held to 80, for
+// half as many warps again, 64 prompt tokens took 7.4 us in place of 4.3). The
+// looks at the list are T entries for each CTA, so a CTA takes more entries where
+// the list is long: 8192 prompt tokens of 8 heads, e4m3, 17.4 us (2.9 TB/s);
+// a decode step of 256 requests 6.3 us.
 #pragma once
+
+#include <algorithm>
 
 #include "q8_common.cuh"
 
 namespace pagedkv {
 
-constexpr int kAppendQ8Warps = 4;
-constexpr int kAppendQ8Run = 16;                   // most entries a warp looks at
+constexpr int kAppendQ8Warps = 8;
+constexpr int kAppendQ8CtasPerSm = 2;
+constexpr int kAppendQ8Run = 256;                  // most entries of a CTA, one per thread
 constexpr float kQ8Tiny = 7.888609052210118e-31f;  // 2^-100: below it a tile counts as zeros (1 / s stays finite)
 
 // Largest magnitude of words of elements, on their bit patterns (which order
@@ -68,13 +72,27 @@ template <> struct Bits<__nv_bfloat16> {
   }
 };
 
-// Warp (4 x + w, head y, kv z) serves the leaders among entries
-// [run * (4 x + w), + run).
+// A CTA's shared memory. Hash table of its blocks, of a power of two of slots, at
+// least four times its entries; then by entry (a block goes by the entry that
+// put it into the table): the latest token of each row, whether the block is led
+// elsewhere, and the list of the blocks that are the CTA's.
+constexpr int32_t kAppendQ8Empty = INT32_MIN;
+struct AppendQ8Shared {
+  int32_t rows[kAppendQ8Run][16];
+  int32_t key[4 * kAppendQ8Run];
+  int32_t owner[4 * kAppendQ8Run];
+  int32_t elsewhere[kAppendQ8Run];
+  int2 lead[kAppendQ8Run];  // entry, block
+  int32_t num_lead;
+};
+
+// CTA (x, y): the blocks first named by entries [run * x, + run), planes
+// [group * y, + group) of the 2 * num_kv_heads (K of every head, then V).
 template <typename T, int D, typename Code>
-__global__ void __launch_bounds__(kAppendQ8Warps * 32, 6)
+__global__ void __launch_bounds__(kAppendQ8Warps * 32, kAppendQ8CtasPerSm)
 append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ pool,
                  const int64_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
-                 Q8Layout lay, int32_t run) {
+                 Q8Layout lay, int32_t run, int32_t group) {
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr int E = 16 / sizeof(T);     // elements per lane and step
   constexpr int kLanes = D / E;         // lanes of a row
@@ -87,56 +105,94 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     uint32_t w[4];
     __device__ __forceinline__ float get(int c) const { return Bits<T>::get(w, c); }
   };
-  __shared__ int32_t row_src[kAppendQ8Warps][16];
-  const int32_t warp = threadIdx.x >> 5;
-  const int32_t lane = threadIdx.x & 31;
-  const int32_t h = blockIdx.y;
-  const int32_t kv = blockIdx.z;
-  const bool reports = h == 0 && kv == 0;
-  const T* src = kv ? v : k;
-  const int32_t t0 = (blockIdx.x * kAppendQ8Warps + warp) * run;
-  if (t0 >= num_tokens) return;
-  // entry t's slot, -1 for padding, a bad slot or an entry outside the list
-  auto slot_of = [&](int64_t t) -> int64_t { return t >= 0 && t < num_tokens ? __ldg(slots + t) : -1; };
-  const int64_t raw0 = slot_of((int64_t)t0 + lane), raw_prev = slot_of((int64_t)t0 - 32 + lane);
-  const int64_t raw1 = slot_of((int64_t)t0 + 32 + lane), raw2 = slot_of((int64_t)t0 + 64 + lane);
-  auto block_of = [&](int64_t s) -> int32_t { return s >= 0 && s < num_slots ? (int32_t)(s >> 4) : -1; };
-  const int32_t b0 = block_of(raw0), b_prev = block_of(raw_prev);
-  if (reports && lane < run && raw0 >= num_slots) raise_device_error(PA_DEVERR_SLOT);
+  __shared__ AppendQ8Shared sh;
+  int32_t table = 32;
+  while (table < 4 * run) table *= 2;
+  const int32_t tid = threadIdx.x;
+  const int32_t warp = tid >> 5;
+  const int32_t lane = tid & 31;
+  const int32_t t0 = blockIdx.x * run;
+  auto hash = [&](int32_t b) -> int32_t { return (int32_t)((uint32_t)b * 2654435761u >> 16) & (table - 1); };
 
-  // leaders: the run's first entry of a block that none of the 31 entries before it names
-  const uint32_t same0 = __match_any_sync(kAll, b0);
-  uint32_t todo = __ballot_sync(kAll, b0 >= 0 && lane < run && (same0 & ((1u << lane) - 1u)) == 0);
+  // the CTA's entries, and the first looks at the list, in flight together
+  constexpr int kLook = 8;
+  int64_t seen[kLook];
+  auto look = [&](int32_t base) {
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const int64_t t = (int64_t)base + i * (kAppendQ8Warps * 32) + tid;
+      seen[i] = t < num_tokens ? __ldg(slots + t) : -1;
+    }
+  };
+  const bool mine = tid < run && tid < num_tokens - t0;
+  const int64_t my_slot = mine ? __ldg(slots + t0 + tid) : -1;
+  look(0);
+  for (int32_t i = tid; i < table; i += kAppendQ8Warps * 32) sh.key[i] = kAppendQ8Empty;
+  for (int32_t i = tid; i < run * 16; i += kAppendQ8Warps * 32) (&sh.rows[0][0])[i] = -1;
+  sh.elsewhere[tid] = 0;
+  if (tid == 0) sh.num_lead = 0;
+  __syncthreads();
+  int32_t my_at = -1;  // this entry's place in the table, where it stands for its block
+  if (my_slot >= num_slots && blockIdx.y == 0) raise_device_error(PA_DEVERR_SLOT);
+  if (my_slot >= 0 && my_slot < num_slots) {
+    const int32_t b = (int32_t)(my_slot >> 4);
+    int32_t at = hash(b);
+    for (;;) {
+      const int32_t was = atomicCAS(sh.key + at, kAppendQ8Empty, b);
+      if (was == kAppendQ8Empty) {
+        sh.owner[at] = tid;
+        my_at = at;
+      }
+      if (was == kAppendQ8Empty || was == b) break;
+      at = (at + 1) & (table - 1);
+    }
+  }
+  __syncthreads();
+  for (int32_t base = 0;;) {
+    int32_t has[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) has[i] = sh.key[hash((int32_t)(seen[i] >> 4))];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      if (has[i] == kAppendQ8Empty) continue;
+      const int64_t s = seen[i];
+      const int32_t b = (int32_t)(s >> 4);
+      int32_t at = hash(b);
+      while (has[i] != b && has[i] != kAppendQ8Empty) {
+        at = (at + 1) & (table - 1);
+        has[i] = sh.key[at];
+      }
+      if (has[i] == b && s >= 0 && s < num_slots) {
+        const int32_t t = base + i * (kAppendQ8Warps * 32) + tid;
+        const int32_t o = sh.owner[at];
+        if (t < t0) sh.elsewhere[o] = 1;
+        else atomicMax(&sh.rows[o][(int32_t)(s & 15)], t);
+      }
+    }
+    if (num_tokens - base <= kLook * kAppendQ8Warps * 32) break;
+    base += kLook * kAppendQ8Warps * 32;
+    look(base);
+  }
+  __syncthreads();
+  if (my_at >= 0 && !sh.elsewhere[tid]) sh.lead[atomicAdd(&sh.num_lead, 1)] = make_int2(tid, sh.key[my_at]);
+  __syncthreads();
+
   const int32_t my_row = lane / kLanes;
   const int32_t my_col = (lane % kLanes) * E;
-  while (todo) {
-    const int32_t first = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int32_t blk = __shfl_sync(kAll, b0, first);
-    if (__any_sync(kAll, b_prev == blk && lane > first)) continue;  // an earlier entry leads
+  const int32_t planes = min(group, 2 * num_kv_heads - (int32_t)blockIdx.y * group);
+  const int32_t tiles = sh.num_lead * planes;
+  const uint32_t stride = (uint32_t)num_kv_heads * D * sizeof(T);  // bytes of a token
+  for (int32_t i = warp; i < tiles; i += kAppendQ8Warps) {
+    const int32_t plane = blockIdx.y * group + i % planes;
+    const int32_t kv = plane >= num_kv_heads, h = plane - kv * num_kv_heads;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>((kv ? v : k) + h * D + my_col);
+    const int2 at = sh.lead[i / planes];
+    const int32_t blk = at.y;
+    const int32_t* row_src = sh.rows[at.x];
     uint8_t* tile = pool + (size_t)blk * lay.block_bytes + ((size_t)kv * num_kv_heads + h) * 16 * D;
     float* scale_at = reinterpret_cast<float*>(pool + q8_scale_at(lay, blk, kv, h, num_kv_heads));
     const float s_old = *scale_at;
-
-    // row -> its latest entry, counted from t0 (-1: not written now), 32 entries at a time
-    __syncwarp();
-    if (lane < 16) row_src[warp][lane] = -1;
-    __syncwarp();
-    int64_t raw = raw0;
-    uint32_t in = __ballot_sync(kAll, b0 == blk);
-    for (int32_t w = 0;;) {
-      const bool member = (in >> lane) & 1u;
-      const int32_t r = member ? (int32_t)(raw & 15) : 32 + lane;
-      const uint32_t same = __match_any_sync(kAll, r);
-      if (member && (same >> lane) == 1u) row_src[warp][r] = 32 * w + lane;
-      __syncwarp();
-      const int32_t last = 31 - __clz(in);  // of this window
-      ++w;
-      raw = w == 1 ? raw1 : w == 2 ? raw2 : slot_of((int64_t)t0 + 32 * w + lane);
-      in = __ballot_sync(kAll, block_of(raw) == blk);
-      if (in == 0 || __ffs(in) + 31 - last > 31) break;
-    }
-    const bool fresh = row_src[warp][0] >= 0;
+    const bool fresh = row_src[0] >= 0;
 
     // rows of steps c0 .. c0 + C - 1
     Words x[C];
@@ -144,11 +200,11 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
     auto load = [&](int c0) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int32_t e = row_src[warp][(c0 + i) * kRows + my_row];
+        const int32_t t = row_src[(c0 + i) * kRows + my_row];
         x[i].q = make_uint4(0, 0, 0, 0);
-        if (e >= 0) {
+        if (t >= 0) {
           written |= 1u << (c0 + i);
-          x[i].q = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(t0 + e) * num_kv_heads + h) * D + my_col));
+          x[i].q = __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)(uint32_t)t * stride));
         }
       }
     };
@@ -242,18 +298,22 @@ append_q8_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __re
 template <typename T, int D, typename Code>
 inline cudaError_t launch_append_q8(const void* k, const void* v, void* pool, const int64_t* slots,
                                     int32_t num_tokens, int32_t num_kv_heads, int32_t num_blocks, cudaStream_t st) {
-  // One entry per warp while all warps are resident at once (24 per SM; a decode
-  // step: every token leads a tile of its own: 256 tokens of 8 heads 5.6 us by
-  // two entries a warp, 6.3 by one); with more, a warp takes a run of entries,
-  // of which a prompt's tokens make one or two tiles.
-  const int64_t tiles = (int64_t)num_tokens * num_kv_heads * 2;
+  // Eight planes a CTA, one for each warp, and as few entries as leave all CTAs
+  // resident at once (8 heads: 2048 prompt tokens 8.5 us by 16 entries, 11.1 by 4,
+  // 12.5 by 64; 8192 tokens 17.5 us by 64, 27.3 by 16; a step of 256 requests 6.3 us
+  // by 2, 6.9 by 1, 8.2 by 4). Lists too long for that get more planes into a CTA,
+  // for fewer looks at the list (131072 tokens 245 us, 371 with eight planes).
+  const int64_t planes = (int64_t)2 * num_kv_heads, resident = (int64_t)kAppendQ8CtasPerSm * device_sm_count();
+  int64_t group = std::min<int64_t>(planes, kAppendQ8Warps);
   int32_t run = 1;
-  while (run < kAppendQ8Run && tiles / run > (int64_t)(run == 1 ? 24 : 64) * device_sm_count()) run *= 2;
-  const int64_t per_cta = (int64_t)run * kAppendQ8Warps;
-  const dim3 grid((unsigned)((num_tokens + per_cta - 1) / per_cta), (unsigned)num_kv_heads, 2);
+  auto chunks = [&]() { return ((int64_t)num_tokens + run - 1) / run; };
+  auto groups = [&]() { return (planes + group - 1) / group; };
+  while (run < kAppendQ8Run && chunks() * groups() > resident) run *= 2;
+  while (group < planes && chunks() * groups() > 2 * resident) group = std::min(2 * group, planes);
+  const dim3 grid((unsigned)chunks(), (unsigned)groups());
   append_q8_kernel<T, D, Code><<<grid, kAppendQ8Warps * 32, 0, st>>>(
       reinterpret_cast<const T*>(k), reinterpret_cast<const T*>(v), reinterpret_cast<uint8_t*>(pool), slots,
-      num_tokens, num_kv_heads, (int64_t)num_blocks * 16, q8_layout(num_kv_heads, D), run);
+      num_tokens, num_kv_heads, (int64_t)num_blocks * 16, q8_layout(num_kv_heads, D), run, (int32_t)group);
   return cudaGetLastError();
 }
 
