@@ -365,10 +365,13 @@ size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads,
  * pa_decode over an 8-bit pool: the same operation, arguments, checks and
  * errors, with K_t and V_t = code * scale. q, out: io_dtype. Products are
  * formed on the codes (exact in fp16) and accumulated in fp32; bf16 queries
- * are exact too (down to 2^-31 of a head's largest element), probabilities are
- * rounded to fp16 (2^-11 relative); fp32 queries and their probabilities keep
- * 22 bits. int8 codes of bf16 queries are summed as code + 128 and the 128s
- * taken off in fp32.
+ * are exact too (down to 2^-31 of a head's largest element), a probability times
+ * its V scale is rounded to fp16 (2^-11 relative, down to 2^-21 of a head's
+ * largest such product); fp32 queries and those products keep 22 bits. Tiles of V
+ * scale 0 count in the sum of the probabilities alone, in fp32. int8 codes of bf16
+ * queries are summed as code + 128 and the 128s taken off in fp32. Where V scales
+ * lie below 2^-96 the output may come out as 0. Table entries behind a sequence's
+ * length may be read; their values do not matter.
  */
 pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
                        const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -381,8 +384,10 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool,
  * pa_prefill over an 8-bit pool: the same operation, arguments, checks and
  * errors, with K_t and V_t = code * scale; q, out bf16. Products are formed on
  * the codes (exact in bf16 and fp16) and accumulated in fp32; a probability
- * times its V scale is rounded to fp16 (2^-11 relative). Where scores pass about
- * 2^25 (off by units in fp32) a row may come out as 0. Supported: head_dim 128,
+ * times its V scale is rounded to fp16 (2^-11 relative, down to 2^-21 of a row's
+ * largest such product). Tiles of V scale 0 count in the sum of the probabilities
+ * alone, in fp32. Where scores pass about 2^25 (off by units in fp32), or V scales
+ * lie below 2^-96, a row may come out as 0. Supported: head_dim 128,
  * num_heads / num_kv_heads in {1, 2, 4, 8, 16}, scale >= 0 (else
  * PA_ERR_INVALID_ARG).
  */

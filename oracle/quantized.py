@@ -105,8 +105,8 @@ def attention(q: np.ndarray, kv: np.ndarray, scale: float, scales: np.ndarray):
     bound() needs, each [n][H][D] or [n][H][1]:
       mag   the sum of p |v|
       big   the largest scale * sum |q_d k_d| over the tokens seen
-      low   the largest p * v_scale (a scale of 0 counts as 1) times the sum of
-            the |V codes|
+      low   the largest p * v_scale times the sum of the |V codes| (tiles of
+            scale 0 aside)
       big1  the largest scale * k_scale * sum |q_d|
       mag1  the sum of p * v_scale"""
     n, H, D = q.shape
@@ -123,8 +123,7 @@ def attention(q: np.ndarray, kv: np.ndarray, scale: float, scales: np.ndarray):
         big[:, h, 0] = np.where(seen, abs(scale) * (np.abs(q[:, h]) @ np.abs(k).T), 0).max(1)
         big1[:, h, 0] = abs(scale) * np.abs(q[:, h]).sum(1) * np.where(seen, ks, 0).max(1)
         mag1[:, h, 0] = p @ vs
-        vs = np.where(vs > 0, vs, 1)
-        low[:, h] = (p * vs).max(1, keepdims=True) * (seen @ (np.abs(v) / vs[:, None]))
+        low[:, h] = (p * vs).max(1, keepdims=True) * (seen @ (np.abs(v) / np.where(vs > 0, vs, 1)[:, None]))
     return out, (mag, big, low, big1, mag1)
 
 

@@ -37,8 +37,10 @@
 // of a score m and a log2 v_b, r: where scores are so large that fp32 spaces
 // them by more than a fraction, x - m is formed first, from rounded x, so that
 // the largest exponent is still what it should be. The same fp32 values of P,
-// before they are rounded, give the sum l += P / v_b. A V scale of 0 counts as
-// 1 there, and its block adds nothing to the output.
+// before they are rounded, give the sum l += P / v_b. A block whose V scale is 0
+// adds nothing to the output, so it stays out of n, which would sink the others'
+// P in fp16: its scores go into a sum of their own, with a reference of its own,
+// that joins l where the warps' states are joined.
 //
 // fp32 queries: q (scaled per head by a power of two) and P are split into two
 // fp16 terms each (22 significand bits), each term its own MMA.
@@ -92,6 +94,7 @@ struct Q8Shared {
   uint64_t bars[kQ8Warps][kQ8Stages];
   float red_m[kQ8Warps][16];
   float red_l[kQ8Warps][16];
+  float2 zero[kQ8Warps][16];  // by head: reference and sum of the warp's blocks of V scale 0
   int32_t next_item;
   int32_t abort;
 };
@@ -227,7 +230,7 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
   const int32_t npre = my < S ? my : S;
   for (int32_t i = 0; i < npre; ++i) issue(i);
 
-  float my_ks = 0.f, my_lv = 0.f, my_rv = 1.f;
+  float my_ks = 0.f, my_lv = -INFINITY, my_rv = 0.f;
   bool has_v = false;
   if (my_ok) {
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.pool);
@@ -308,49 +311,14 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
     }
   };
   clear();
+  if (lane < 16) sh.zero[warp][lane] = make_float2(kQ8NoRef, 0.f);
+  __syncwarp();
   const int32_t row = lane & 15;  // of this lane's ldmatrix address
   const uint32_t row_addr = wsm_addr + Tile::chunk(row, lane >> 4);
 
-  for (int32_t i = 0; i < my; ++i) {
-    const int32_t s = i % S;
-    const bool arrived = mbar_wait_bounded(&sh.bars[warp][s], (phase >> s) & 1u, kWaitLimitNs);
-    if (__any_sync(0xffffffffu, !arrived)) {
-      // as in decode_partition: report, let the copies in flight land, drop this warp's state
-      if (lane == 0) raise_device_error(PA_DEVERR_TIMEOUT);
-      const int32_t issued = min(i + S, my);
-      for (int32_t k = i; k < issued; ++k) {
-        const int32_t sk = k % S;
-        mbar_wait_bounded(&sh.bars[warp][sk], (phase >> sk) & 1u, kWaitLimitNs);
-        phase ^= 1u << sk;
-      }
-      clear();
-      if (lane == 0) sh.abort = 1;
-      break;
-    }
-    phase ^= 1u << s;
-    const int32_t nvalid = min(16, t1 - (t0 + (rank + i * W) * 16));
-    const float ks = __shfl_sync(0xffffffffu, my_ks, i);
-    const float lv = __shfl_sync(0xffffffffu, my_lv, i);
-    const float rv = __shfl_sync(0xffffffffu, my_rv, i);
-    if (nvalid < 16 || !((v_mask >> i) & 1u)) {
-      // What must not count becomes zero codes: both tiles of a block that was
-      // not loaded, the V tile under a zero scale, and the V rows behind the
-      // sequence's end (they may hold NaN codes, which a zero probability does
-      // not silence).
-      uint8_t* stg = wsm + s * Tile::kStage;
-      const bool loaded = (ok_mask >> i) & 1u;
-      const int32_t from = (v_mask >> i) & 1u ? nvalid : 0;
-      for (int32_t e = lane; e < Tile::kStage / 16; e += 32) {
-        const int32_t kv = e / (Tile::kBytes / 16), t = e / (D / 16) % 16, c = e % (D / 16);
-        if (!loaded || (kv == 1 && t >= from))
-          *reinterpret_cast<uint4*>(stg + kv * Tile::kBytes + Tile::chunk(t, c)) = make_uint4(0, 0, 0, 0);
-      }
-      __syncwarp();
-    }
-
-    // S^T: rows = tokens (gid, gid + 8), columns = heads (2 tig, 2 tig + 1)
-    const uint32_t at = row_addr + s * Tile::kStage;
-    float sc[NT][4], sc2[NT][4];  // even and odd k-steps: two shorter chains of dependent MMAs
+  // S^T of the block at `at`: rows = tokens (gid, gid + 8), columns = heads (2 tig, 2 tig + 1)
+  auto scores = [&](uint32_t at, float (&sc)[NT][4]) {
+    float sc2[NT][4];  // odd k-steps: two shorter chains of dependent MMAs
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -377,6 +345,74 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[nt][e] += sc2[nt][e];
+  };
+
+  for (int32_t i = 0; i < my; ++i) {
+    const int32_t s = i % S;
+    const bool arrived = mbar_wait_bounded(&sh.bars[warp][s], (phase >> s) & 1u, kWaitLimitNs);
+    if (__any_sync(0xffffffffu, !arrived)) {
+      // as in decode_partition: report, let the copies in flight land, drop this warp's state
+      if (lane == 0) raise_device_error(PA_DEVERR_TIMEOUT);
+      const int32_t issued = min(i + S, my);
+      for (int32_t k = i; k < issued; ++k) {
+        const int32_t sk = k % S;
+        mbar_wait_bounded(&sh.bars[warp][sk], (phase >> sk) & 1u, kWaitLimitNs);
+        phase ^= 1u << sk;
+      }
+      clear();
+      if (lane == 0) sh.abort = 1;
+      break;
+    }
+    phase ^= 1u << s;
+    const int32_t nvalid = min(16, t1 - (t0 + (rank + i * W) * 16));
+    const float ks = __shfl_sync(0xffffffffu, my_ks, i);
+    const float lv = __shfl_sync(0xffffffffu, my_lv, i);
+    const float rv = __shfl_sync(0xffffffffu, my_rv, i);
+    const bool no_v = !((v_mask >> i) & 1u);  // lv is -inf: all of P is 0
+    if (nvalid < 16 || no_v) {
+      // What must not count becomes zero codes: both tiles of a block that was
+      // not loaded, the V tile under a zero scale, and the V rows behind the
+      // sequence's end (they may hold NaN codes, which a zero probability does
+      // not silence).
+      uint8_t* stg = wsm + s * Tile::kStage;
+      const bool loaded = (ok_mask >> i) & 1u;
+      const int32_t from = no_v ? 0 : nvalid;
+      for (int32_t e = lane; e < Tile::kStage / 16; e += 32) {
+        const int32_t kv = e / (Tile::kBytes / 16), t = e / (D / 16) % 16, c = e % (D / 16);
+        if (!loaded || (kv == 1 && t >= from))
+          *reinterpret_cast<uint4*>(stg + kv * Tile::kBytes + Tile::chunk(t, c)) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (no_v) {
+        float zs[NT][4];
+        scores(row_addr + s * Tile::kStage, zs);
+        // the block's share of the sum, in the units of l: 2^(reference - lift)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float2* z = &sh.zero[warp][8 * nt + 2 * tig + j];
+            const float f = sfac[nt][j] * ks;
+            const float y0 = gid < nvalid ? __fmul_rn(zs[nt][j] - qsum[nt][j], f) : -INFINITY;
+            const float y1 = gid + 8 < nvalid ? __fmul_rn(zs[nt][j + 2] - qsum[nt][j], f) : -INFINITY;
+            float zm = fmaxf(fmaxf(y0, y1), z->x);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, off));
+            float zl = (ex2_ftz(y0 - zm) + ex2_ftz(y1 - zm)) * 128.f;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) zl += __shfl_xor_sync(0xffffffffu, zl, off);
+            zl = fmaf(z->y, ex2_ftz(z->x - zm), zl);
+            __syncwarp();
+            if (gid == 0) *z = make_float2(zm, zl);
+          }
+        }
+        __syncwarp();
+      }
+    }
+
+    const uint32_t at = row_addr + s * Tile::kStage;
+    float sc[NT][4];
+    scores(at, sc);
     // the exponents x + log2 v_b - (m + r) + lift
     float x[NT][4];
     auto exponents = [&]() {
@@ -513,7 +549,10 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
         ls += __shfl_xor_sync(0xffffffffu, ls, 8);
         ls += __shfl_xor_sync(0xffffffffu, ls, 16);
         const int32_t head = 8 * nt + 2 * tig + j;
-        const float inv = 1.f / ls;
+        const float n = m[nt][j] + r[nt][j];
+        const float2 z = sh.zero[warp][head];
+        const float M = fmaxf(n, z.x), f = exp2f(n - M);
+        const float inv = f / fmaf(ls, f, z.y * exp2f(z.x - M));
         if (head < G) {
           T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * H + (size_t)g * G + head) * D + 2 * gid;
 #pragma unroll
@@ -555,12 +594,14 @@ __device__ __forceinline__ void decode_q8_partition(const CUtensorMap& tmap, con
     const int32_t h = threadIdx.x;
     float M = kQ8NoRef;
 #pragma unroll
-    for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sh.red_m[w][h]);
+    for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, fmaxf(sh.red_m[w][h], sh.zero[w][h].x));
     float e[kQ8Warps], Ls = 0.f;
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) {
       e[w] = exp2f(sh.red_m[w][h] - M);  // 0 for a warp that had no block
       Ls = fmaf(sh.red_l[w][h], e[w], Ls);
+      const float2 z = sh.zero[w][h];
+      Ls = fmaf(z.y, exp2f(z.x - M), Ls);
     }
     const float f = nparts == 1 ? 1.f / Ls : 1.f;
 #pragma unroll

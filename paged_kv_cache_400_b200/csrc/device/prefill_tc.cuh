@@ -70,8 +70,10 @@
 // x + log2 v_b, and P, at most 2^15, goes to fp16 (2^-11 relative, against 2^-8
 // of bf16; V's conversion from int8 takes 5 instructions per 4 codes instead of
 // 8, from e4m3 2 instead of 10: 512-token chunks behind 4096 tokens 356 -> 345
-// us with int8, 361 -> 341 us with e4m3). Zero V scales count as 1 over a
-// zeroed tile. m lies 2^-22 of itself above the maximum: huge scores, which fp32
+// us with int8, 361 -> 341 us with e4m3). A block of V scale 0 stays out of m and
+// P; its scores go into a sum of their own, with a reference of its own, that joins
+// l at the row's end (350 -> 361 us in that case, whose blocks all have a scale: the
+// softmax loop has no registers left for it). m lies 2^-22 of itself above the maximum: huge scores, which fp32
 // spaces by more than a unit, then cannot push an exponent past fp16 (from
 // scores of about 2^25 on, where they are off by units, rows come out as 0).
 #pragma once
@@ -91,6 +93,7 @@ constexpr int kTcHalfBytes = kTcKeys * 128;       // 64 keys x 64 dims x bf16
 constexpr int kTcStageBytes = 4 * kTcHalfBytes;   // K lo, K hi, V lo, V hi
 constexpr int kTcQBytes = 128 * 256;              // one 128-row query tile x 128 dims x bf16
 constexpr float kTcRescaleLog2 = 8.0f;            // raise the reference max past this growth
+constexpr float kTcNoRef = -1e30f;                // reference before any score was seen (finite: n - n stays 0)
 constexpr float kTcLift = 7.0f;                   // 8-bit pools: P is held 2^7 above its reference, at most 2^15 in fp16
 
 // Two query tiles of 128 rows share every staged KV tile: one CTA per SM (all
@@ -119,7 +122,9 @@ struct TcUnit {
 
 template <int kQTiles, int kStages, bool kQ8>
 struct PrefillTcShared {
-  float4 block_scale[kQ8 ? kStages : 1][kTcBlocksPerTile];  // scale k_b log2 e, log2 v_b, 1 / v_b of each staged block
+  // scale k_b log2 e, log2 v_b (-inf where v_b is 0), 1 / v_b (0 there) of each staged block
+  float4 block_scale[kQ8 ? kStages : 1][kTcBlocksPerTile];
+  alignas(4) uint8_t no_v[kQ8 ? kStages : 1][kTcBlocksPerTile];  // v_b is 0
   alignas(16) uint4 clc_resp;    // response of the last cancellation request
   int32_t unit_desc[2][6];       // published units (TcUnit), two slots
   uint64_t clc_bar;              // cancellation response written
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             if (in && lane == 0) raise_device_error(PA_DEVERR_BLOCK);
 #pragma unroll
             for (int i = 0; i < 8; ++i) code[i] = make_uint4(0, 0, 0, 0);
-            ks = vs = 1.f;
+            ks = vs = in ? 0.f : 1.f;
           }
         };
         load_codes(0);
@@ -480,6 +485,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
 #pragma unroll
           for (int i = 0; i < 8; ++i) c[i] = code[i];
           const float k_b = ks, v_b = vs;
+          const bool has_v = v_b > 0.f;
           if (j + 1 < nt_max) load_codes(j + 1);
           if (J >= (uint32_t)S) {
             const bool ok = mbar_wait_bounded(&sh.kv_empty[s], (J / S - 1) & 1u, kWaitLimitNs);
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
           }
           // V rows that must not count: under a zero scale, and behind the
           // sequence's end (they may hold NaN codes, which P = 0 does not silence)
-          const int32_t live = v_b == 0.f ? 0 : u.L - (j * kTcBlocksPerTile + pw) * 16;
+          const int32_t live = !has_v ? 0 : u.L - (j * kTcBlocksPerTile + pw) * 16;
           if (live < 16) {
 #pragma unroll
             for (int i = 4; i < 8; ++i)
@@ -514,9 +520,11 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             *reinterpret_cast<uint4*>(line + ((ch ^ (key & 7)) << 4)) = lo;
             *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (key & 7)) << 4)) = hi;
           }
-          if (lane == 0)
-            sh.block_scale[s][pw] = make_float4(p.scale_log2 * k_b, v_b > 0.f ? log2f(v_b) : 0.f,
-                                                v_b > 0.f ? 1.f / v_b : 1.f, 0.f);
+          if (lane == 0) {
+            sh.no_v[s][pw] = !has_v;
+            sh.block_scale[s][pw] = has_v ? make_float4(p.scale_log2 * k_b, log2f(v_b), 1.f / v_b, 0.f)
+                                          : make_float4(p.scale_log2 * k_b, -INFINITY, 0.f, 0.f);
+          }
           fence_proxy_async_smem();  // the stage's writes before the MMAs read them
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.kv_full[s]);
@@ -850,6 +858,13 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
       const bool valid = tok < te;
       const int32_t P = valid ? ctx + tok : ctx + te - 1;  // padding rows: any finite row
       float m_ref = -INFINITY, l = 0.f;
+      // 8-bit: reference and sum of the blocks of V scale 0; in memory, as they are rare
+      // and registers are not
+      volatile float zero[2];
+      if constexpr (kQ8) {
+        zero[0] = kTcNoRef;
+        zero[1] = 0.f;
+      }
       for (int32_t j = 0; j < ntt; ++j) {
         const uint32_t JS = js + (uint32_t)j;
         const bool arrived = mbar_wait_bounded(&sh.s_full[t][JS & 1], (JS >> 1) & 1u, kWaitLimitNs);
@@ -885,7 +900,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             m4[c >> 3] = max3(m4[c >> 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
-          mt = -INFINITY;
+          mt = kTcNoRef;
 #pragma unroll
           for (int b = 0; b < kTcBlocksPerTile; ++b)
             mt = fmaxf(mt, fmaf(m4[b], bsc[b].x, bsc[b].y));
@@ -896,6 +911,28 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
             m4[c & 3] = max3(m4[c & 3], __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
           mt = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
           mt *= p.scale_log2;
+        }
+        if constexpr (kQ8) {
+          if (*reinterpret_cast<const uint32_t*>(sh.no_v[(jkv + (uint32_t)j) % S])) {
+            float zm = zero[0], zl = zero[1];
+#pragma unroll
+            for (int b = 0; b < kTcBlocksPerTile; ++b) {
+              if (sh.no_v[(jkv + (uint32_t)j) % S][b]) {
+                const float f = bsc[b].x;
+                float top = zm;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  if (key0 + 16 * b + c <= P) top = fmaxf(top, __uint_as_float(sr[16 * b + c]) * f);
+                zl *= ex2_sfu(zm - top);
+                zm = top;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  if (key0 + 16 * b + c <= P) zl += ex2_sfu(__uint_as_float(sr[16 * b + c]) * f - zm);
+              }
+            }
+            zero[0] = zm;
+            zero[1] = zl;
+          }
         }
         if (j == 0) {
           m_ref = mt;  // key 0 is never masked: finite
@@ -978,7 +1015,14 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
           // tile (its rows after the new tokens belong to the next sequence)
           // by plain stores, each warp its own valid rows. The warps of the
           // group meet on mbarriers, so that every wait is bounded.
-          const float inv = kQ8 && !(l > 0.f) ? (l == 0.f ? 0.f : l) : 1.f / l;
+          float inv = kQ8 && !(l > 0.f) ? (l == 0.f ? 0.f : l) : 1.f / l;
+          if constexpr (kQ8) {
+            const float zm = zero[0], zl = zero[1];
+            if (zl != 0.f) {  // in units of 2^zm, l of 2^(m_ref - lift)
+              const float M = fmaxf(m_ref, zm), f = exp2f(m_ref - M);
+              inv = f / fmaf(l, f, 128.f * zl * exp2f(zm - M));
+            }
+          }
           const bool whole = te == tb + QT;
           const int32_t row0 = (warp & 3) * 32;
           uint4* out4 = reinterpret_cast<uint4*>(p.out);
