@@ -337,8 +337,8 @@ int64_t pa_pool_block_bytes(pa_pool_desc pool);
  *   - its row 0 is among them: the tile starts afresh with scale A * (1/M), and
  *     rows it is not given in this call hold no tokens any more;
  *   - otherwise the scale s only grows. int8: max(s, A * (1/M)). e4m3: s if
- *     A <= s * M, else s * 2^k with the smallest k that makes A / (s * M) <=
- *     2^k (A * (1/M) where s is 0). Where it grew, all rows of the tile not
+ *     A <= s * M, else s * 2^k with the smallest k that makes A <= s * M * 2^k
+ *     (A * (1/M) where s is 0). Where it grew, all rows of the tile not
  *     written now are coded again: code(value(c) * (s / s')).
  *   - a new element x becomes the code nearest to x * (1/s'), ties to even.
  * Error of an element, with s the tile's scale when it is read: int8 at most

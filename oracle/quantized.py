@@ -50,8 +50,8 @@ def grown(s: F32, a: F32, code: str) -> F32:
         return s
     if s == 0:
         return a * inv
-    m, e = np.frexp(a / room)                                # a / room = m 2^e, m in [0.5, 1)
-    return F32(np.ldexp(s, int(e - 1 if m == F32(0.5) else e)))
+    (ma, ea), (mr, er) = np.frexp(a), np.frexp(room)         # m 2^e, m in [0.5, 1)
+    return F32(np.ldexp(s, int(ea) - int(er) + int(ma > mr)))
 
 
 def append(codes: np.ndarray, scales: np.ndarray, k: np.ndarray, v: np.ndarray, slots, code: str) -> None:

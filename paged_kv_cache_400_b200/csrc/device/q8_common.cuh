@@ -68,10 +68,11 @@ struct CodeE4m3 {
     const float room = __fmul_rn(s, kMax);
     if (!(a > room)) return s;
     if (s == 0.f) return __fmul_rn(a, kInvMax);
-    // smallest k with 2^k >= a / room
-    const uint32_t r = __float_as_uint(__fdiv_rn(a, room));
-    const int32_t k = (int32_t)(r >> 23) - 127 + ((r & 0x7fffffu) ? 1 : 0);
-    return ldexpf(s, k);
+    // smallest k with room * 2^k >= a, from exponents and significands: the quotient
+    // of the two may be more than fp32 holds
+    int32_t ea, er;
+    const float ma = frexpf(a, &ea), mr = frexpf(room, &er);
+    return ldexpf(s, ea - er + (ma > mr ? 1 : 0));
   }
   __device__ __forceinline__ static uint32_t encode(float x) {
     uint16_t h;
