@@ -341,10 +341,13 @@ int64_t pa_pool_block_bytes(pa_pool_desc pool);
  *     (A * (1/M) where s is 0). Where it grew, all rows of the tile not
  *     written now are coded again: code(value(c) * (s / s')).
  *   - a new element x becomes the code nearest to x * (1/s'), ties to even.
- * Error of an element, with s the tile's scale when it is read: int8 at most
- * s/2 when the tile was written in one call, and at most s/2 more for each
- * call that made s grow afterwards; e4m3 2^-4 relative (2^-10 * s absolute
- * below the smallest normal), whether or not s grew.
+ * Error of an element x, with s the tile's scale when it is read: int8 at most
+ * s/2 when the tile was written in one call, and at most s/2 more for each call
+ * that made s grow afterwards. e4m3: at most the larger of 2^-4 |x| and 2^-10 s
+ * when s did not grow afterwards, and at most 2^-4 |x| + 2^-9 s however often it
+ * did (a growth adds half a step of the smallest numbers, 2^-10 of its new scale,
+ * and each scale is at least twice the one before). All but for the fp32
+ * roundings of x * (1/s), 2^-22 of |x|.
  * A NaN is stored as 0 and an infinity as the largest code of its sign (0 in a
  * tile whose scale is 0), and either sets PA_DEVERR_NONFINITE.
  * k, v: device, [num_tokens][num_kv_heads][head_dim] contiguous, io_dtype,

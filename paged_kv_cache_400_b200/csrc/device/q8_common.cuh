@@ -43,7 +43,8 @@ __device__ __forceinline__ size_t q8_scale_at(const Q8Layout& l, int64_t blk, in
 //                     larger than needed costs every element. e4m3 grows by a
 //                     power of two: its error is relative, so the larger scale
 //                     costs nothing, and coding the kept rows again is exact
-//                     but for values that fall below the smallest normal.
+//                     but for values that fall below the smallest normal, by
+//                     half a step there (2^-10 of the grown scale).
 struct CodeInt8 {
   static constexpr float kMax = 127.0f;
   static constexpr float kInvMax = 1.0f / 127.0f;
