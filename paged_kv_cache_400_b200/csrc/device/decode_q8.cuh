@@ -79,7 +79,6 @@ struct Q8Tile {
   static constexpr int kStages = kQ8Stages;
   static constexpr int kRing = kStages * kStage;     // per warp
   static constexpr int kSmem = kQ8Warps * kRing + 1024;
-  static constexpr int kCtasPerSm = D == 128 ? 3 : 5;  // by shared memory, and by registers for groups of up to 8 heads
   // Byte offset of 16-byte chunk c of token t in a tile, 128-byte swizzle: the
   // chunk's place in its line is XORed with the line's index, so the 8 rows of
   // an ldmatrix fall in 8 different bank groups for both head sizes.
@@ -835,9 +834,45 @@ inline cudaError_t launch_decode_q8_merge(const DecodeParams& p, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, decode_q8_merge_kernel<T, D, kSplit>, p);
 }
 
-// CTAs that are resident at once (where a group has up to 8 heads).
-inline int32_t q8_resident(int32_t head_dim) {
-  return (head_dim == 128 ? Q8Tile<128>::kCtasPerSm : Q8Tile<64>::kCtasPerSm) * device_sm_count();
+// CTAs of a decode kernel that an SM holds, with the kernel's shared-memory limit
+// set; asked of the device once.
+template <typename T, int D, int NT, typename Code>
+inline cudaError_t q8_ctas_per_sm(int32_t* per_sm) {
+  static PerDevice<int32_t> occupancy;
+  return occupancy.get(per_sm, [](int32_t* v) {
+    auto kernel = decode_q8_kernel<T, D, NT, Code>;
+    int32_t n = 0;
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Tile<D>::kSmem);
+    if (r == cudaSuccess)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kQ8Warps * 32, Q8Tile<D>::kSmem);
+    *v = n > 0 ? n : 1;
+    return r;
+  });
+}
+
+// CTAs that are resident at once on the current device; a B200's where no device
+// can be asked (sizing a workspace on a host without a GPU). What fits is decided
+// by shared memory for head_dim 128 and up to 8 heads a group (3), by registers
+// elsewhere (64: 4; 9 to 16 heads: 2 or 3).
+template <typename T, int D, int NT, typename Code>
+inline int32_t q8_resident_of() {
+  int32_t n = 0;
+  if (q8_ctas_per_sm<T, D, NT, Code>(&n) != cudaSuccess) {
+    cudaGetLastError();  // clear the error of a failed query
+    constexpr bool bf16 = sizeof(T) == 2, e4m3 = std::is_same<Code, CodeE4m3>::value;
+    n = NT == 1 ? (D == 64 ? 4 : 3) : bf16 && (D == 128 || e4m3) ? 3 : 2;
+  }
+  return n * device_sm_count();
+}
+inline int32_t q8_resident(int32_t head_dim, int32_t group, int32_t dtype, int32_t io_dtype) {
+  auto of = [&](auto io, auto code) {
+    using T = decltype(io);
+    using Code = decltype(code);
+    if (head_dim == 64) return group <= 8 ? q8_resident_of<T, 64, 1, Code>() : q8_resident_of<T, 64, 2, Code>();
+    return group <= 8 ? q8_resident_of<T, 128, 1, Code>() : q8_resident_of<T, 128, 2, Code>();
+  };
+  auto of_code = [&](auto code) { return io_dtype == PA_BF16 ? of(__nv_bfloat16{}, code) : of(float{}, code); };
+  return dtype == PA_Q8_INT8 ? of_code(CodeInt8{}) : of_code(CodeE4m3{});
 }
 // A warp per (sequence, KV head) where sequences are short and pairs many: 200
 // sequences x 8 heads of up to 137 tokens take 10.5 us by warps and 23.8 us by
@@ -846,6 +881,12 @@ inline int32_t q8_resident(int32_t head_dim) {
 inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
   return max_seq_len <= kQ8WarpTokens && pairs >= (int64_t)3 * device_sm_count();
 }
+// CTAs from which the work list pays: four rounds of them for head_dim 64, whose
+// items are shorter beside the list's launch, three for 128 (64: 64 x 8 heads,
+// 3.5 rounds, lognormal up to 8192 34.1 us without the list and its partitions,
+// 38.2 with them, all of 8192 105 and 113, uniform 76 and 73. 128: 48 x 8, 3.5
+// rounds, 41.9 and 41.2, 142 and 142, 94 and 88).
+inline int64_t q8_list_from(int32_t head_dim, int64_t resident) { return (head_dim == 64 ? 4 : 3) * resident; }
 // Tokens of a partition, a multiple of 16, at most 2048: when every sequence
 // has the longest length, the resident CTAs take one partition each, or as many
 // as 2048 tokens make necessary (one request of 131071 tokens and 8 heads: two
@@ -854,31 +895,31 @@ inline bool q8_by_warp(int64_t pairs, int32_t max_seq_len) {
 // (230 tokens: 5.9 us, in two partitions 6.3 us). Two rounds throughout were
 // slower on batches of even lengths (6 x 8 heads of 2928 tokens: 15.0 us by one
 // round, 19.1 by two) and faster on ragged ones (28 x 2 of up to 10517: 23.0 and
-// 18.7 us). Batches of three to ten rounds of 2048 tokens, taken from the list,
+// 18.7 us). Batches of up to ten rounds of 2048 tokens, taken from the list,
 // get 1024: their lengths are ragged as a rule, and the longest items would end
 // alone (64 x 8 heads, lognormal up to 8192: 42.8 us, by 2048 tokens 51.7; all of
 // 8192: 174.5 and 174.8). Beyond ten rounds 2048 are enough and cheaper (256 x 8:
 // 121 us, by 1024 tokens 130), and sequences that fit one partition are not cut
 // (64 x 32 of up to 2048: 99 and 106 us).
-inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
+inline int32_t q8_partition_tokens(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int64_t resident,
+                                   int32_t max_seq_len) {
   const int64_t pairs = std::max<int64_t>((int64_t)num_seqs * num_kv_heads, 1);
   if (q8_by_warp(pairs, max_seq_len)) return kQ8WarpTokens;  // one partition
-  const int64_t resident = q8_resident(head_dim);
   const int64_t least = ((int64_t)max_seq_len + 2047) / 2048;  // partitions a sequence needs
   const int64_t rounds = std::max<int64_t>((least * pairs + resident - 1) / resident, 1);
   const int64_t parts = std::max<int64_t>(rounds * resident / pairs, 1);
   const int64_t tokens = (((int64_t)max_seq_len + parts - 1) / parts + 15) / 16 * 16;
   const int64_t smallest = max_seq_len <= 256 ? 256 : 128;
-  const bool some_rounds = pairs * least > 3 * resident && pairs * least <= 10 * resident;
+  const bool some_rounds = pairs * least > q8_list_from(head_dim, resident) && pairs * least <= 10 * resident;
   const int64_t most = least > 1 && some_rounds ? 1024 : 2048;
   return (int32_t)std::min<int64_t>(std::max<int64_t>(tokens, smallest), most);
 }
-// The plan kernel's list from more than three rounds of CTAs on: it saves the
+// The plan kernel's list from more than so many rounds of CTAs on: it saves the
 // empty CTAs of ragged batches and starts the longest partitions first, but is a
 // launch more (182 x 2 heads of 4608 tokens, 2.5 rounds: 80.3 us without, 84.5
 // with it).
-inline bool q8_use_list(int64_t pairs, int32_t partitions, int32_t head_dim) {
-  return partitions >= 2 && pairs * partitions > (int64_t)3 * q8_resident(head_dim);
+inline bool q8_use_list(int64_t pairs, int32_t partitions, int32_t head_dim, int64_t resident) {
+  return partitions >= 2 && pairs * partitions > q8_list_from(head_dim, resident);
 }
 
 // Tensor map of an 8-bit pool's codes: (byte of a 128-byte line, line of the
@@ -921,15 +962,8 @@ inline pa_status launch_decode_q8(const DecodeParams& p, cudaStream_t st) {
     return PA_OK;
   }
   auto kernel = decode_q8_kernel<T, D, NT, Code>;
-  static PerDevice<int32_t> occupancy;  // resident CTAs per SM, with the shared-memory limit set once per device
   int32_t per_sm = 1;
-  cudaError_t e = occupancy.get(&per_sm, [&](int32_t* v) {
-    int32_t n = 0;
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Tile<D>::kSmem);
-    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kQ8Warps * 32, Q8Tile<D>::kSmem);
-    *v = n > 0 ? n : 1;
-    return r;
-  });
+  cudaError_t e = q8_ctas_per_sm<T, D, NT, Code>(&per_sm);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode_q8: %s", cudaGetErrorString(e));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -557,9 +557,14 @@ pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool, c
 
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads, pa_pool_desc pool, int32_t max_seq_len) {
   if (num_seqs <= 0 || num_heads <= 0 || max_seq_len <= 0 || pool.num_kv_heads <= 0 || pool.head_dim <= 0) return 0;
-  return workspace_layout(num_seqs, num_heads, pool, max_seq_len,
-                          pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, max_seq_len))
-      .total;
+  // for either type of the queries
+  size_t most = 0;
+  for (int32_t io : {PA_BF16, PA_F32}) {
+    const int32_t resident = pagedkv::q8_resident(pool.head_dim, num_heads / pool.num_kv_heads, pool.dtype, io);
+    const int32_t S = pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, resident, max_seq_len);
+    most = std::max(most, workspace_layout(num_seqs, num_heads, pool, max_seq_len, S).total);
+  }
+  return most;
 }
 
 pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int32_t* block_tables,
@@ -575,7 +580,8 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int3
     return fail(PA_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 65535", fn, pool.num_kv_heads);
   if (num_seqs == 0) return PA_OK;
   const int32_t len = max_seq_len > 0 ? max_seq_len : 1;
-  const int32_t S = pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, len);
+  const int32_t resident = pagedkv::q8_resident(pool.head_dim, num_heads / pool.num_kv_heads, pool.dtype, io_dtype);
+  const int32_t S = pagedkv::q8_partition_tokens(num_seqs, pool.num_kv_heads, pool.head_dim, resident, len);
   if (((int64_t)len + S - 1) / S > kMaxPartitions)
     return fail(PA_ERR_UNSUPPORTED, "%s: max_seq_len %d needs more than %lld partitions of %d tokens", fn, max_seq_len,
                 (long long)kMaxPartitions, S);
@@ -585,7 +591,8 @@ pa_status pa_decode_q8(void* out, const void* q, const void* kv_pool, const int3
   if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
   char* ws = reinterpret_cast<char*>(workspace);
-  const bool use_list = pagedkv::q8_use_list((int64_t)num_seqs * pool.num_kv_heads, w.partitions, pool.head_dim);
+  const bool use_list =
+      pagedkv::q8_use_list((int64_t)num_seqs * pool.num_kv_heads, w.partitions, pool.head_dim, resident);
   pagedkv::DecodeParams p = {};
   p.out = out;
   p.q = q;
