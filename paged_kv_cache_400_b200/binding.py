@@ -551,7 +551,8 @@ def make_free_ring(num_blocks: int, order=None, device="cuda"):
     """(free_ring, ring_state) of a pool whose blocks are all free, handed out
     in `order` (0, 1, ... by default)."""
     ring = torch.arange(num_blocks, dtype=torch.int32) if order is None else torch.as_tensor(order, dtype=torch.int32)
-    if ring.shape != (num_blocks,):
+    blocks = torch.arange(num_blocks, dtype=torch.int32)
+    if ring.shape != (num_blocks,) or not torch.equal(ring.sort().values.cpu(), blocks):
         raise ValueError("order must name every block once")
     return ring.to(device), torch.tensor([0, num_blocks, 0, 0], dtype=torch.int32, device=device)
 
