@@ -360,7 +360,8 @@ pa_status pa_reshape_and_cache_q8(const void* k, const void* v, void* kv_pool,
                                   const int64_t* slot_mapping, int32_t num_tokens,
                                   pa_pool_desc pool, int32_t io_dtype, void* stream);
 
-/* Bytes of device workspace pa_decode_q8 needs; as pa_decode_workspace_size. */
+/* Bytes of device workspace pa_decode_q8 needs, with either io_dtype; as
+ * pa_decode_workspace_size. */
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_heads,
                                    pa_pool_desc pool, int32_t max_seq_len);
 

@@ -858,13 +858,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
       const bool valid = tok < te;
       const int32_t P = valid ? ctx + tok : ctx + te - 1;  // padding rows: any finite row
       float m_ref = -INFINITY, l = 0.f;
-      // 8-bit: reference and sum of the blocks of V scale 0; in memory, as they are rare
-      // and registers are not
-      volatile float zero[2];
-      if constexpr (kQ8) {
-        zero[0] = kTcNoRef;
-        zero[1] = 0.f;
-      }
+      float zm = kTcNoRef, zl = 0.f;  // 8-bit: reference and sum of the blocks of V scale 0
       for (int32_t j = 0; j < ntt; ++j) {
         const uint32_t JS = js + (uint32_t)j;
         const bool arrived = mbar_wait_bounded(&sh.s_full[t][JS & 1], (JS >> 1) & 1u, kWaitLimitNs);
@@ -913,8 +907,7 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
           mt *= p.scale_log2;
         }
         if constexpr (kQ8) {
-          if (*reinterpret_cast<const uint32_t*>(sh.no_v[(jkv + (uint32_t)j) % S])) {
-            float zm = zero[0], zl = zero[1];
+          if (__builtin_expect(*reinterpret_cast<const uint32_t*>(sh.no_v[(jkv + (uint32_t)j) % S]) != 0u, 0)) {
 #pragma unroll
             for (int b = 0; b < kTcBlocksPerTile; ++b) {
               if (sh.no_v[(jkv + (uint32_t)j) % S][b]) {
@@ -930,8 +923,6 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
                   if (key0 + 16 * b + c <= P) zl += ex2_sfu(__uint_as_float(sr[16 * b + c]) * f - zm);
               }
             }
-            zero[0] = zm;
-            zero[1] = zl;
           }
         }
         if (j == 0) {
@@ -1017,7 +1008,6 @@ __global__ void __launch_bounds__(TcConfig<kQTiles, !std::is_void<Code>::value>:
           // group meet on mbarriers, so that every wait is bounded.
           float inv = kQ8 && !(l > 0.f) ? (l == 0.f ? 0.f : l) : 1.f / l;
           if constexpr (kQ8) {
-            const float zm = zero[0], zl = zero[1];
             if (zl != 0.f) {  // in units of 2^zm, l of 2^(m_ref - lift)
               const float M = fmaxf(m_ref, zm), f = exp2f(m_ref - M);
               inv = f / fmaf(l, f, 128.f * zl * exp2f(zm - M));
