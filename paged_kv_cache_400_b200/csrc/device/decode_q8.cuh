@@ -50,10 +50,10 @@
 // sequence), or resident CTAs that take them from the plan kernel's list, or a
 // warp per (sequence, KV head); a merge kernel joins the partitions.
 //
-// Measured: 256 requests of lognormal lengths (32 heads over 8, int8) 121 us,
-// 5.9 TB/s of the pool's bytes; 64 requests with 32 KV heads, e4m3, 99 us, 6.4
-// TB/s, as much as a copy reaches. What is left in the first is the launches of
-// plan and merge (8 us) and the ends of the items.
+// Measured: 256 requests of lognormal lengths (32 heads over 8, int8) 121 to 128 us
+// by machine, 5.6 to 5.9 TB/s of the pool's bytes; 64 requests with 32 KV heads,
+// e4m3, 99 to 113 us, 5.6 to 6.4 TB/s, up to what a copy reaches. What is left in
+// the first is the launches of plan and merge (8 us) and the ends of the items.
 #pragma once
 
 #include <algorithm>

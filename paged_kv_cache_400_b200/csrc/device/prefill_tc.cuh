@@ -72,7 +72,7 @@
 // 8, from e4m3 2 instead of 10: 512-token chunks behind 4096 tokens 356 -> 345
 // us with int8, 361 -> 341 us with e4m3). A block of V scale 0 stays out of m and
 // P; its scores go into a sum of their own, with a reference of its own, that joins
-// l at the row's end (350 -> 361 us in that case, whose blocks all have a scale: the
+// l at the row's end (350 -> 360 us in that case, whose blocks all have a scale: the
 // softmax loop has no registers left for it). m lies 2^-22 of itself above the maximum: huge scores, which fp32
 // spaces by more than a unit, then cannot push an exponent past fp16 (from
 // scores of about 2^25 on, where they are off by units, rows come out as 0).
